@@ -18,14 +18,45 @@ SYMBOLS = (
     "bpe_strerror",
 )
 
+# every symbol include/bpe_lm.h declares
+LM_SYMBOLS = (
+    "bpe_embed", "bpe_embed_grad_workspace_bytes", "bpe_embed_grad", "bpe_process_logits",
+    "bpe_block_tables_workspace_bytes", "bpe_block_tables",
+)
+
 BPE_OK, BPE_EINVAL, BPE_EMERGES, BPE_EIDMAP, BPE_EWORKSPACE, BPE_EHIP, BPE_ENOMEM, BPE_ENOTSUP, \
     BPE_EFORMAT, BPE_ESCRATCH = 0, -1, -2, -3, -4, -5, -6, -7, -8, -9
 NOALLOC_SCRATCH_BYTES = 128 << 20
 STATUS_BAD_DOC_OFFSETS, STATUS_IDS_CAPACITY, STATUS_BAD_ID, STATUS_BYTES_CAPACITY, \
     STATUS_BAD_ID_OFFSETS = 1, 2, 4, 8, 16
+STATUS_NO_BLOCKS, STATUS_TABLE_FULL, STATUS_BAD_LENGTH, STATUS_BAD_MASK_ROW, STATUS_BAD_BIAS = \
+    32, 64, 128, 256, 512
+F32, BF16, F16 = 0, 1, 2
+MAX_WIDTH = 1 << 18
+MAX_ROWS = 1 << 27
 OP_ENCODE, OP_DECODE = 0, 1
 MAX_MERGES = 1 << 20
 MAX_ID = (1 << 24) - 1
+
+
+
+class LogitsArgs(C.Structure):
+    """bpe_logits_args of include/bpe_lm.h."""
+    _fields_ = [
+        ("logits", C.c_void_p), ("logits_stride", C.c_int64),
+        ("rows", C.c_int64), ("vocab", C.c_int64),
+        ("prompt_ids", C.c_void_p), ("n_prompt", C.c_int64), ("prompt_off", C.c_void_p),
+        ("made_ids", C.c_void_p), ("made_width", C.c_int64), ("made_stride", C.c_int64),
+        ("made_len", C.c_void_p),
+        ("repetition", C.c_void_p), ("frequency", C.c_void_p), ("presence", C.c_void_p),
+        ("bias_ids", C.c_void_p), ("bias_values", C.c_void_p), ("n_bias", C.c_int64),
+        ("bias_off", C.c_void_p),
+        ("mask", C.c_void_p), ("n_masks", C.c_int64), ("mask_stride", C.c_int64),
+        ("mask_row", C.c_void_p),
+        ("out", C.c_void_p), ("out_stride", C.c_int64), ("status", C.c_void_p),
+        ("logits_type", C.c_int32), ("out_type", C.c_int32),
+    ]
+
 
 _lib = None
 
@@ -80,5 +111,19 @@ def load() -> C.CDLL:
     L.bpe_stage_times.restype = i32
     L.bpe_strerror.argtypes = [i32]
     L.bpe_strerror.restype = C.c_char_p
+    f32 = C.c_float
+    L.bpe_embed.argtypes = [p, i32, i64, i64, i64, p, i64, f32, i32, p, i32, i64, p, p]
+    L.bpe_embed.restype = i32
+    L.bpe_embed_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    L.bpe_embed_grad_workspace_bytes.restype = sz
+    L.bpe_embed_grad.argtypes = [p, i32, i64, p, i64, i64, i64, f32, i32, i32, p, i32, i64, p, sz,
+                                 p, p]
+    L.bpe_embed_grad.restype = i32
+    L.bpe_process_logits.argtypes = [C.POINTER(LogitsArgs), p]
+    L.bpe_process_logits.restype = i32
+    L.bpe_block_tables_workspace_bytes.argtypes = [i64]
+    L.bpe_block_tables_workspace_bytes.restype = sz
+    L.bpe_block_tables.argtypes = [p, i64, i64, p, p, i64, p, i64, i64, i32, p, p, p, p, p, sz, p, p]
+    L.bpe_block_tables.restype = i32
     _lib = L
     return L

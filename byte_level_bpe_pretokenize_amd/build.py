@@ -15,6 +15,9 @@ LIB = os.path.join(PKG, "libbpe.so")
 SOURCES = [os.path.join(CSRC, f)
            for f in ("bpe_encode.hip", "bpe_decode.hip", "bpe_train.hip", "bpe_noalloc.hip",
                      "bpe_api.cpp", "bpe_tables.cpp", "bpe_text.cpp")]
+# the operators on token IDs (include/bpe_lm.h)
+SOURCES += [os.path.join(PKG, "csrc_lm", f)
+            for f in ("lm_embed.hip", "lm_logits.hip", "lm_blocks.hip", "lm_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,0 +1,106 @@
+// lm_internal.h -- arguments and layouts shared by the host checks (lm_api.cpp)
+// and the kernels of the operators on token IDs.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/bpe_lm.h"
+
+namespace bpe {
+
+// Workgroups of one launch, at most (a launch has fewer than 2^32 threads, of
+// up to 256 a workgroup).
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;
+
+// ---- embedding ---------------------------------------------------------------
+struct EmbedArgs {
+  const void *weight;
+  const int32_t *ids;
+  void *out;
+  int32_t *status;
+  int64_t n_rows, n_ids, w_stride, o_stride;
+  int32_t width;
+  int32_t pad_id;
+  float scale;
+  uint32_t units;   // vectors per row
+  uint32_t magic;   // 2^31 / units + 1: x / units = x * magic >> 31 while x * units < 2^31
+};
+
+hipError_t launch_embed(const EmbedArgs &a, int wt, int ot, hipStream_t stream);
+
+// ---- the embedding's gradient ----------------------------------------------
+// The IDs are sorted (a stable radix sort of at most kDigitBits bits per pass,
+// tiles of kSortTile IDs); the sorted list is cut into tiles of `tile` IDs, one
+// wave per tile and 64 vectors of columns.
+constexpr int kEmbedUnits = 1024;  // vectors per workgroup of the forward
+constexpr int kZeroRows = 16;      // rows of the table per workgroup of zeros
+constexpr int kDigitBits = 9;
+constexpr int kMaxDigits = 1 << kDigitBits;
+constexpr int kSortThreads = 1024;
+constexpr int kSortTile = 4096;
+
+struct GradArgs {
+  const void *grad;
+  const int32_t *ids;
+  void *out;
+  int32_t *status;
+  int64_t n_rows, n_ids, g_stride, o_stride;
+  int32_t width;
+  int32_t pad_id;
+  float scale;
+  int32_t accumulate;
+  // workspace
+  int32_t *key[2], *pos[2];  // sorted IDs (n_rows: adds nothing) and their positions
+  int32_t *counts;           // [sort tiles][digits]
+  uint8_t *touched;          // [n_rows] 1: the ID occurs
+  float *part;               // [tiles][2][width] sums of rows that a tile's edge cuts
+  // launch
+  int32_t sort_tiles, passes, bits;  // bits of one pass's digit
+  int32_t tile;                      // IDs per tile of the sums
+  int32_t tiles;
+  int32_t slabs;                     // column groups of 64 vectors
+  int64_t sum_blocks;
+};
+
+struct GradLayout {
+  size_t key0, key1, pos0, pos1, counts, touched, part, total;
+  int32_t sort_tiles, passes, bits, tile, tiles;
+};
+
+GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width);
+hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);
+
+// ---- logits ------------------------------------------------------------------
+constexpr int kLogitSlab = 4096;  // logits per workgroup
+
+hipError_t launch_logits(const bpe_logits_args &a, hipStream_t stream);
+
+// ---- block tables --------------------------------------------------------------
+struct BlockArgs {
+  const int64_t *off;
+  int64_t R, T;
+  const int32_t *cached, *free_blocks;
+  int64_t n_free;
+  int32_t *table;
+  int64_t width, stride;
+  int32_t bs;
+  uint32_t magic;     // x / bs = (x * magic) >> shift for 0 <= x < 2^31
+  int32_t shift;
+  int64_t *slots;
+  int32_t *positions, *lengths;
+  int64_t *used;
+  int32_t *status;
+  int64_t *first;     // [R] workspace: blocks taken before r within its group
+  int64_t *gsum;      // [kBlockGroups] workspace: blocks taken by each group
+  int32_t group_log2; // requests per group
+};
+
+constexpr int kBlockChunk = 2048;     // new tokens per workgroup
+constexpr int kBlockGroups = 256;     // groups of requests, at most
+constexpr int kBlockFused = 2048;     // requests that each workgroup sums by itself
+constexpr int kBlockScan = 1024;      // threads of the scan: requests per step
+
+hipError_t launch_blocks(const BlockArgs &a, hipStream_t stream);
+
+}  // namespace bpe

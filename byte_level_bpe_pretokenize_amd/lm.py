@@ -1,0 +1,369 @@
+"""Operators on token IDs at the two ends of a language model, over the C ABI
+in include/bpe_lm.h (argument marshalling only).
+
+``embed`` / ``embed_grad`` / ``embedding``: rows of an embedding table by the
+IDs that ``Model.encode_batch`` gives, scaled, and the table's gradient.
+``process_logits``: penalties for repeated tokens, biases and grammar masks on
+the logits of the next token.  ``block_tables``: block tables, slots and
+positions of a paged cache from the requests' lengths.
+
+Every call takes ``status``, an int32 device tensor of one element that the
+caller has cleared: the call ORs _lib.STATUS_* bits into it and does not
+synchronize.  Without one the call makes its own, waits for it, and raises
+where a bit is set.  Work goes to ``stream``, or the current stream.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import _lib
+from .api import BPEError
+
+_TYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
+
+
+def _type(t: torch.dtype, what: str) -> int:
+    try:
+        return _TYPES[t]
+    except KeyError:
+        raise TypeError(f"{what}: float32, bfloat16 or float16 expected, got {t}") from None
+
+
+def _flat(t: torch.Tensor, dtype: torch.dtype, what: str) -> int:
+    """The pointer of a contiguous tensor (0 where it is empty)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, what: str) -> int:
+    """The row stride of a matrix whose rows are consecutive elements."""
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a matrix, got {t.dim()} dimensions")
+    n, m = t.shape
+    if m > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: expected rows of consecutive elements")
+    if n > 1:
+        s = t.stride(0)
+        if s < m:
+            raise ValueError(f"{what}: expected rows that do not overlap")
+        return s
+    return m
+
+
+def _int32(x: int, lo: int, what: str) -> int:
+    if not lo <= x < 1 << 31:
+        raise ValueError(f"{what}: {x} is out of range")
+    return int(x)
+
+
+class _Call:
+    """One call: its device, stream and status.  Temporaries and outputs are
+    allocated on the call's stream, and inputs marked as used there, so that
+    memory freed after the call is not handed out while its kernels run."""
+
+    def __init__(self, name: str, tensors, status, stream):
+        self.name = name
+        if not torch.cuda.is_available():
+            raise RuntimeError("libbpe needs a HIP device; none is visible")
+        device = torch.device("cuda", torch.cuda.current_device())
+        for t in tensors:
+            if t is not None and t.device != device:
+                raise ValueError(f"{name}: expected tensors on the current device ({device}), "
+                                 f"got one on {t.device}")
+        here = torch.cuda.current_stream(device)
+        self.device, self.stream, self.status = device, here if stream is None else stream, status
+        self.other = None
+        if stream is not None and stream != here:
+            self.other = torch.cuda.stream(stream)
+            self.other.__enter__()
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        self.own = status is None
+        if self.own:
+            self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        elif status.dtype != torch.int32 or status.numel() != 1:
+            self.leave()
+            raise TypeError("status: int32 tensor of one element expected")
+
+    def empty(self, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def leave(self):
+        if self.other is not None:
+            self.other.__exit__(None, None, None)
+            self.other = None
+
+    def end(self, rc: int):
+        if rc != _lib.BPE_OK:
+            raise BPEError(rc, f"bpe_{self.name}")
+        if self.own:
+            st = int(self.status.item())
+            if st:
+                raise RuntimeError(f"bpe_{self.name} device status {st:#x}")
+
+
+def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id: int = -1,
+          out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+          status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """bpe_embed: ``scale * weight[ids]``, zeros where an ID is ``pad_id``.
+
+    weight (V, D); ids int32, contiguous, any shape; returns ids.shape + (D,)
+    of ``out_dtype`` (the weight's by default), or ``out``, a matrix of
+    ids.numel() rows, filled."""
+    pad_id = _int32(pad_id, -1, "pad_id")
+    wt = _type(weight.dtype, "weight")
+    ws = _rows(weight, "weight")
+    ip = _flat(ids, torch.int32, "ids")
+    n, (V, D) = ids.numel(), weight.shape
+    if out is None:
+        dt = weight.dtype if out_dtype is None else out_dtype
+        ot, os_ = _type(dt, "out_dtype"), D
+    else:
+        ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
+        if tuple(out.shape) != (n, D) or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out: ({n}, {D}) of out_dtype expected, got {tuple(out.shape)}")
+    call = _Call("embed", (weight, ids, out, status), status, stream)
+    try:
+        res = call.empty((*ids.shape, D), dt) if out is None else out
+        rc = _lib.load().bpe_embed(weight.data_ptr(), wt, V, D, ws, ip, n, scale, pad_id,
+                                   res.data_ptr(), ot, os_, call.status.data_ptr(),
+                                   call.stream.cuda_stream)
+        call.end(rc)
+    finally:
+        call.leave()
+    return res
+
+
+def embed_grad_workspace_bytes(n_ids: int, n_rows: int, width: int) -> int:
+    return int(_lib.load().bpe_embed_grad_workspace_bytes(n_ids, n_rows, width))
+
+
+def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float = 1.0, *,
+               pad_id: int = -1, out: torch.Tensor | None = None,
+               out_dtype: torch.dtype | None = None, accumulate: bool = False,
+               workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """bpe_embed_grad: the gradient of ``embed``'s weight, (n_rows, D).
+
+    grad: the gradient of embed's result, ids.shape + (D,) or (ids.numel(), D);
+    returns ``out`` (added to with ``accumulate``) or a new matrix of
+    ``out_dtype`` (float32 by default).  ``workspace``: a contiguous device
+    tensor of embed_grad_workspace_bytes bytes, allocated by the call when left
+    out."""
+    pad_id = _int32(pad_id, -1, "pad_id")
+    gt = _type(grad.dtype, "grad")
+    ip = _flat(ids, torch.int32, "ids")
+    n = ids.numel()
+    if grad.dim() != 2:
+        if grad.shape[:-1] != ids.shape:
+            raise ValueError(f"grad: {tuple(ids.shape)} + (width,) expected, got {tuple(grad.shape)}")
+        if not grad.is_contiguous():
+            raise ValueError("grad: expected a contiguous tensor or a matrix")
+        grad = grad.view(n, grad.shape[-1])
+    gs, D = _rows(grad, "grad"), grad.shape[1]
+    if grad.shape[0] != n:
+        raise ValueError(f"grad: {n} rows expected, got {grad.shape[0]}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        dt = torch.float32 if out_dtype is None else out_dtype
+        ot, os_ = _type(dt, "out_dtype"), D
+    else:
+        ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
+        if tuple(out.shape) != (n_rows, D) or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out: ({n_rows}, {D}) of out_dtype expected, got {tuple(out.shape)}")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    call = _Call("embed_grad", (grad, ids, out, workspace, status), status, stream)
+    try:
+        L = _lib.load()
+        res = call.empty((n_rows, D), dt) if out is None else out
+        if workspace is None:
+            need = L.bpe_embed_grad_workspace_bytes(n, n_rows, D)
+            workspace = call.empty(max(need, 1), torch.uint8)
+        rc = L.bpe_embed_grad(grad.data_ptr(), gt, gs, ip, n, n_rows, D, scale, pad_id,
+                              1 if accumulate else 0, res.data_ptr(), ot, os_,
+                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                              call.status.data_ptr(), call.stream.cuda_stream)
+        call.end(rc)
+    finally:
+        call.leave()
+    return res
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, weight, ids, scale, pad_id, out_dtype, status):
+        ctx.save_for_backward(ids)
+        ctx.embed = (weight.shape[0], weight.dtype, scale, pad_id, status)
+        return embed(weight, ids, scale, pad_id=pad_id, out_dtype=out_dtype, status=status)
+
+    @staticmethod
+    def backward(ctx, grad):
+        (ids,) = ctx.saved_tensors
+        n_rows, dtype, scale, pad_id, status = ctx.embed
+        g = embed_grad(grad.contiguous(), ids, n_rows, scale, pad_id=pad_id, out_dtype=dtype,
+                       status=status)
+        return g, None, None, None, None, None
+
+
+def embedding(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id: int = -1,
+              out_dtype: torch.dtype | None = None,
+              status: torch.Tensor | None = None) -> torch.Tensor:
+    """``embed`` with ``embed_grad`` as its gradient for autograd (a dense
+    gradient of the weight's type), on the current stream."""
+    return _Embedding.apply(weight, ids, scale, pad_id, out_dtype, status)
+
+
+def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = None,
+                   prompt_off: torch.Tensor | None = None, out_ids: torch.Tensor | None = None,
+                   out_len: torch.Tensor | None = None, repetition: torch.Tensor | None = None,
+                   frequency: torch.Tensor | None = None, presence: torch.Tensor | None = None,
+                   bias_off: torch.Tensor | None = None, bias_ids: torch.Tensor | None = None,
+                   bias_values: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                   mask_row: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   out_dtype: torch.dtype | None = None, status: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """bpe_process_logits: the processed logits, (B, V), of ``out_dtype`` (the
+    logits' by default); ``out`` may be ``logits`` itself.
+
+    prompt_ids, prompt_off: each row's prompt, ragged as Model.encode_batch
+    gives it (int32, int64 (B + 1)).  out_ids (B, M) int32, out_len (B) int32:
+    what each row has generated so far.  repetition, frequency, presence:
+    float32 (B).  bias_off int64 (B + 1), bias_ids int32 (increasing within a
+    row), bias_values float32.  mask (M, ceil(V / 32)) int32, bit v & 31 of word
+    v >> 5 set where token v may come; mask_row (B) int32, -1 for none."""
+    lt, ls = _type(logits.dtype, "logits"), _rows(logits, "logits")
+    B, V = logits.shape
+
+    def of(t, dtype, n, what):
+        if t is None:
+            return None
+        p = _flat(t, dtype, what)
+        if t.numel() != n:
+            raise ValueError(f"{what}: {n} entries expected, got {t.numel()}")
+        return p
+
+    def together(what, *ts):
+        if any((t is None) != (ts[0] is None) for t in ts):
+            raise ValueError(f"{what} come together")
+
+    together("prompt_ids and prompt_off", prompt_ids, prompt_off)
+    together("out_ids and out_len", out_ids, out_len)
+    together("bias_off, bias_ids and bias_values", bias_off, bias_ids, bias_values)
+    together("mask and mask_row", mask, mask_row)
+    n_prompt = 0 if prompt_ids is None else prompt_ids.numel()
+    n_bias = 0 if bias_ids is None else bias_ids.numel()
+    pp = of(prompt_ids, torch.int32, n_prompt, "prompt_ids")
+    po = of(prompt_off, torch.int64, B + 1, "prompt_off")
+    m_ptr, m_width, m_stride = None, 0, 0
+    if out_ids is not None:
+        if out_ids.dtype != torch.int32:
+            raise TypeError(f"out_ids: torch.int32 expected, got {out_ids.dtype}")
+        m_stride = _rows(out_ids, "out_ids")
+        if out_ids.shape[0] != B:
+            raise ValueError(f"out_ids: {B} rows expected, got {out_ids.shape[0]}")
+        m_ptr, m_width = out_ids.data_ptr(), out_ids.shape[1]
+    k_ptr, k_rows, k_stride = None, 0, 0
+    if mask is not None:
+        if mask.dtype not in (torch.int32, torch.uint32):
+            raise TypeError(f"mask: torch.int32 expected, got {mask.dtype}")
+        k_stride = _rows(mask, "mask")
+        if mask.shape[1] != (V + 31) // 32:
+            raise ValueError(f"mask: {(V + 31) // 32} words a row expected, got {mask.shape[1]}")
+        k_ptr, k_rows = mask.data_ptr(), mask.shape[0]
+    if out is None:
+        dt = logits.dtype if out_dtype is None else out_dtype
+        ot, os_ = _type(dt, "out_dtype"), V
+    else:
+        ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
+        if out.shape != logits.shape or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out: {tuple(logits.shape)} of out_dtype expected, got {tuple(out.shape)}")
+    args = (of(out_len, torch.int32, B, "out_len"),
+            of(repetition, torch.float32, B, "repetition"),
+            of(frequency, torch.float32, B, "frequency"),
+            of(presence, torch.float32, B, "presence"),
+            of(bias_ids, torch.int32, n_bias, "bias_ids"),
+            of(bias_values, torch.float32, n_bias, "bias_values"), n_bias,
+            of(bias_off, torch.int64, B + 1, "bias_off"),
+            k_ptr, k_rows, k_stride, of(mask_row, torch.int32, B, "mask_row"))
+    call = _Call("process_logits",
+                 (logits, prompt_ids, prompt_off, out_ids, out_len, repetition, frequency,
+                  presence, bias_off, bias_ids, bias_values, mask, mask_row, out, status),
+                 status, stream)
+    try:
+        res = call.empty((B, V), dt) if out is None else out
+        a = _lib.LogitsArgs(logits.data_ptr(), ls, B, V, pp, n_prompt, po, m_ptr, m_width,
+                            m_stride, *args, res.data_ptr(), os_, call.status.data_ptr(), lt, ot)
+        call.end(_lib.load().bpe_process_logits(C.byref(a), call.stream.cuda_stream))
+    finally:
+        call.leave()
+    return res
+
+
+def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
+                 free_blocks: torch.Tensor, table: torch.Tensor, block_size: int, *,
+                 slots: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                 lengths: torch.Tensor | None = None, used: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                 stream=None):
+    """bpe_block_tables: enters the blocks that the new tokens need into
+    ``table`` (in place) and returns (slots int64 (n_new), positions int32
+    (n_new), lengths int32 (R), used int64 (1)), new or the tensors given.
+
+    new_off int64 (R + 1): the new tokens' offsets (Model.encode_batch's
+    id_off), n_new of them; cached int32 (R): tokens already in the cache;
+    free_blocks int32: the blocks to take, in order; table int32 (R, W)."""
+    op = _flat(new_off, torch.int64, "new_off")
+    cp = _flat(cached, torch.int32, "cached")
+    fp = _flat(free_blocks, torch.int32, "free_blocks")
+    R = cached.numel()
+    if new_off.numel() != R + 1:
+        raise ValueError(f"new_off: {R + 1} entries expected, got {new_off.numel()}")
+    if table.dtype != torch.int32:
+        raise TypeError(f"table: torch.int32 expected, got {table.dtype}")
+    ts = _rows(table, "table")
+    if table.shape[0] != R:
+        raise ValueError(f"table: {R} rows expected, got {table.shape[0]}")
+    for t, dtype, n, what in ((slots, torch.int64, n_new, "slots"),
+                              (positions, torch.int32, n_new, "positions"),
+                              (lengths, torch.int32, R, "lengths"), (used, torch.int64, 1, "used")):
+        if t is not None:
+            _flat(t, dtype, what)
+            if t.numel() != n:
+                raise ValueError(f"{what}: {n} entries expected, got {t.numel()}")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    block_size = _int32(block_size, 1, "block_size")
+    if n_new < 0:
+        raise ValueError(f"n_new: {n_new} is out of range")
+    call = _Call("block_tables", (new_off, cached, free_blocks, table, slots, positions, lengths,
+                                  used, workspace, status), status, stream)
+    try:
+        L = _lib.load()
+        if slots is None:
+            slots = call.empty(n_new, torch.int64)
+        if positions is None:
+            positions = call.empty(n_new, torch.int32)
+        if lengths is None:
+            lengths = call.empty(R, torch.int32)
+        if used is None:
+            used = call.empty(1, torch.int64)
+        if workspace is None:
+            workspace = call.empty(max(L.bpe_block_tables_workspace_bytes(R), 1), torch.uint8)
+        rc = L.bpe_block_tables(op, R, n_new, cp, fp, free_blocks.numel(), table.data_ptr(),
+                                table.shape[1], ts, block_size, slots.data_ptr(),
+                                positions.data_ptr(), lengths.data_ptr(), used.data_ptr(),
+                                workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(),
+                                call.status.data_ptr(), call.stream.cuda_stream)
+        call.end(rc)
+    finally:
+        call.leave()
+    return slots, positions, lengths, used
