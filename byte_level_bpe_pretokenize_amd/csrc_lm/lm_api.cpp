@@ -176,7 +176,7 @@ int bpe_process_logits(const bpe_logits_args *args, void *hip_stream) {
 }
 
 size_t bpe_block_tables_workspace_bytes(int64_t n_requests) {
-  if (n_requests <= 0) return 0;
+  if (n_requests <= kBlockFused) return 0;
   return (size_t)n_requests * 8 + kBlockGroups * 8;
 }
 
@@ -191,7 +191,8 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
       !stride_ok(table_stride, table_width) || !d_status || !d_used ||
       (n_new > 0 && n_requests == 0) || (n_free > 0 && !d_free_blocks))
     return BPE_EINVAL;
-  if (n_requests > 0 && (!d_new_off || !d_cached || !d_lengths || !d_workspace ||
+  if (n_requests > 0 && (!d_new_off || !d_cached || !d_lengths ||
+                         (n_requests > kBlockFused && !d_workspace) ||
                          (table_width > 0 && !d_table)))
     return BPE_EINVAL;
   if (n_new > 0 && (!d_slots || !d_positions)) return BPE_EINVAL;
@@ -218,8 +219,10 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
   a.lengths = d_lengths;
   a.used = d_used;
   a.status = d_status;
-  a.first = (int64_t *)d_workspace;
-  a.gsum = a.first + n_requests;
+  if (n_requests > kBlockFused) {
+    a.first = (int64_t *)d_workspace;
+    a.gsum = a.first + n_requests;
+  }
   a.group_log2 = 10;
   while (((n_requests - 1) >> a.group_log2) + 1 > kBlockGroups) ++a.group_log2;
   return launch_blocks(a, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;

@@ -24,6 +24,12 @@ from .api import BPEError
 _TYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
 
 
+# the current stream's handle by device index; a stream object costs 20 times
+# as much, more than all the checks of a call
+_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda dev: torch.cuda.current_stream(dev).cuda_stream
+
+
 def _type(t: torch.dtype, what: str) -> int:
     try:
         return _TYPES[t]
@@ -61,51 +67,47 @@ def _int32(x: int, lo: int, what: str) -> int:
     return int(x)
 
 
-class _Call:
-    """One call: its device, stream and status.  Temporaries and outputs are
-    allocated on the call's stream, and inputs marked as used there, so that
-    memory freed after the call is not handed out while its kernels run."""
+def _device(name: str, *tensors) -> int:
+    """The current device's index; refuses tensors that are elsewhere."""
+    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
+        raise RuntimeError("libbpe needs a HIP device; none is visible")
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: expected tensors on the current device (cuda:{dev}), "
+                             f"got one on {t.device}")
+    return dev
 
-    def __init__(self, name: str, tensors, status, stream):
-        self.name = name
-        if not torch.cuda.is_available():
-            raise RuntimeError("libbpe needs a HIP device; none is visible")
-        device = torch.device("cuda", torch.cuda.current_device())
+
+def _status(status: torch.Tensor | None, dev: int) -> torch.Tensor:
+    if status is None:
+        return torch.zeros(1, dtype=torch.int32, device=dev)
+    if status.dtype != torch.int32 or status.numel() != 1:
+        raise TypeError("status: int32 tensor of one element expected")
+    return status
+
+
+def _end(name: str, rc: int, own: torch.Tensor | None) -> None:
+    """Raises what the call refused or, where it has a status of its own, what
+    the device found."""
+    if rc != _lib.BPE_OK:
+        raise BPEError(rc, name)
+    if own is not None:
+        st = int(own.item())
+        if st:
+            raise RuntimeError(f"{name} device status {st:#x}")
+
+
+def _on(stream, call, tensors, *args, **kw):
+    """The call with `stream` as the current stream: what it allocates belongs
+    to that stream, and the tensors given to it are marked as used there, so
+    that no memory freed after the call is handed out while its kernels run."""
+    with torch.cuda.stream(stream):
+        res = call(*args, **kw)
         for t in tensors:
-            if t is not None and t.device != device:
-                raise ValueError(f"{name}: expected tensors on the current device ({device}), "
-                                 f"got one on {t.device}")
-        here = torch.cuda.current_stream(device)
-        self.device, self.stream, self.status = device, here if stream is None else stream, status
-        self.other = None
-        if stream is not None and stream != here:
-            self.other = torch.cuda.stream(stream)
-            self.other.__enter__()
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-        self.own = status is None
-        if self.own:
-            self.status = torch.zeros(1, dtype=torch.int32, device=device)
-        elif status.dtype != torch.int32 or status.numel() != 1:
-            self.leave()
-            raise TypeError("status: int32 tensor of one element expected")
-
-    def empty(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
-
-    def leave(self):
-        if self.other is not None:
-            self.other.__exit__(None, None, None)
-            self.other = None
-
-    def end(self, rc: int):
-        if rc != _lib.BPE_OK:
-            raise BPEError(rc, f"bpe_{self.name}")
-        if self.own:
-            st = int(self.status.item())
-            if st:
-                raise RuntimeError(f"bpe_{self.name} device status {st:#x}")
+            if t is not None:
+                t.record_stream(stream)
+    return res
 
 
 def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id: int = -1,
@@ -116,6 +118,9 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
     weight (V, D); ids int32, contiguous, any shape; returns ids.shape + (D,)
     of ``out_dtype`` (the weight's by default), or ``out``, a matrix of
     ids.numel() rows, filled."""
+    if stream is not None:
+        return _on(stream, embed, (weight, ids, out, status), weight, ids, scale, pad_id=pad_id,
+                   out=out, out_dtype=out_dtype, status=status)
     pad_id = _int32(pad_id, -1, "pad_id")
     wt = _type(weight.dtype, "weight")
     ws = _rows(weight, "weight")
@@ -128,15 +133,12 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
         ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
         if tuple(out.shape) != (n, D) or out_dtype not in (None, out.dtype):
             raise ValueError(f"out: ({n}, {D}) of out_dtype expected, got {tuple(out.shape)}")
-    call = _Call("embed", (weight, ids, out, status), status, stream)
-    try:
-        res = call.empty((*ids.shape, D), dt) if out is None else out
-        rc = _lib.load().bpe_embed(weight.data_ptr(), wt, V, D, ws, ip, n, scale, pad_id,
-                                   res.data_ptr(), ot, os_, call.status.data_ptr(),
-                                   call.stream.cuda_stream)
-        call.end(rc)
-    finally:
-        call.leave()
+    dev = _device("embed", weight, ids, out, status)
+    st = _status(status, dev)
+    res = torch.empty((*ids.shape, D), dtype=dt, device=dev) if out is None else out
+    rc = _lib.load().bpe_embed(weight.data_ptr(), wt, V, D, ws, ip, n, scale, pad_id,
+                               res.data_ptr(), ot, os_, st.data_ptr(), _stream(dev))
+    _end("bpe_embed", rc, st if status is None else None)
     return res
 
 
@@ -156,6 +158,10 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float 
     ``out_dtype`` (float32 by default).  ``workspace``: a contiguous device
     tensor of embed_grad_workspace_bytes bytes, allocated by the call when left
     out."""
+    if stream is not None:
+        return _on(stream, embed_grad, (grad, ids, out, workspace, status), grad, ids, n_rows,
+                   scale, pad_id=pad_id, out=out, out_dtype=out_dtype, accumulate=accumulate,
+                   workspace=workspace, status=status)
     pad_id = _int32(pad_id, -1, "pad_id")
     gt = _type(grad.dtype, "grad")
     ip = _flat(ids, torch.int32, "ids")
@@ -180,20 +186,20 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float 
             raise ValueError(f"out: ({n_rows}, {D}) of out_dtype expected, got {tuple(out.shape)}")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    call = _Call("embed_grad", (grad, ids, out, workspace, status), status, stream)
-    try:
-        L = _lib.load()
-        res = call.empty((n_rows, D), dt) if out is None else out
-        if workspace is None:
-            need = L.bpe_embed_grad_workspace_bytes(n, n_rows, D)
-            workspace = call.empty(max(need, 1), torch.uint8)
-        rc = L.bpe_embed_grad(grad.data_ptr(), gt, gs, ip, n, n_rows, D, scale, pad_id,
-                              1 if accumulate else 0, res.data_ptr(), ot, os_,
-                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                              call.status.data_ptr(), call.stream.cuda_stream)
-        call.end(rc)
-    finally:
-        call.leave()
+    dev = _device("embed_grad", grad, ids, out, workspace, status)
+    L = _lib.load()
+    st = _status(status, dev)
+    res = torch.empty((n_rows, D), dtype=dt, device=dev) if out is None else out
+    if workspace is None:
+        w_bytes = L.bpe_embed_grad_workspace_bytes(n, n_rows, D)
+        workspace = torch.empty(w_bytes, dtype=torch.uint8, device=dev) if w_bytes else None
+    else:
+        w_bytes = workspace.numel() * workspace.element_size()
+    rc = L.bpe_embed_grad(grad.data_ptr(), gt, gs, ip, n, n_rows, D, scale, pad_id,
+                          1 if accumulate else 0, res.data_ptr(), ot, os_,
+                          None if workspace is None else workspace.data_ptr(), w_bytes,
+                          st.data_ptr(), _stream(dev))
+    _end("bpe_embed_grad", rc, st if status is None else None)
     return res
 
 
@@ -239,6 +245,12 @@ def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = No
     float32 (B).  bias_off int64 (B + 1), bias_ids int32 (increasing within a
     row), bias_values float32.  mask (M, ceil(V / 32)) int32, bit v & 31 of word
     v >> 5 set where token v may come; mask_row (B) int32, -1 for none."""
+    if stream is not None:
+        kw = dict(prompt_ids=prompt_ids, prompt_off=prompt_off, out_ids=out_ids, out_len=out_len,
+                  repetition=repetition, frequency=frequency, presence=presence,
+                  bias_off=bias_off, bias_ids=bias_ids, bias_values=bias_values, mask=mask,
+                  mask_row=mask_row, out=out, status=status)
+        return _on(stream, process_logits, (logits, *kw.values()), logits, out_dtype=out_dtype, **kw)
     lt, ls = _type(logits.dtype, "logits"), _rows(logits, "logits")
     B, V = logits.shape
 
@@ -293,17 +305,14 @@ def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = No
             of(bias_values, torch.float32, n_bias, "bias_values"), n_bias,
             of(bias_off, torch.int64, B + 1, "bias_off"),
             k_ptr, k_rows, k_stride, of(mask_row, torch.int32, B, "mask_row"))
-    call = _Call("process_logits",
-                 (logits, prompt_ids, prompt_off, out_ids, out_len, repetition, frequency,
-                  presence, bias_off, bias_ids, bias_values, mask, mask_row, out, status),
-                 status, stream)
-    try:
-        res = call.empty((B, V), dt) if out is None else out
-        a = _lib.LogitsArgs(logits.data_ptr(), ls, B, V, pp, n_prompt, po, m_ptr, m_width,
-                            m_stride, *args, res.data_ptr(), os_, call.status.data_ptr(), lt, ot)
-        call.end(_lib.load().bpe_process_logits(C.byref(a), call.stream.cuda_stream))
-    finally:
-        call.leave()
+    dev = _device("process_logits", logits, prompt_ids, prompt_off, out_ids, out_len, repetition,
+                  frequency, presence, bias_off, bias_ids, bias_values, mask, mask_row, out, status)
+    st = _status(status, dev)
+    res = torch.empty((B, V), dtype=dt, device=dev) if out is None else out
+    a = _lib.LogitsArgs(logits.data_ptr(), ls, B, V, pp, n_prompt, po, m_ptr, m_width, m_stride,
+                        *args, res.data_ptr(), os_, st.data_ptr(), lt, ot)
+    rc = _lib.load().bpe_process_logits(C.byref(a), _stream(dev))
+    _end("bpe_process_logits", rc, st if status is None else None)
     return res
 
 
@@ -320,6 +329,11 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
     new_off int64 (R + 1): the new tokens' offsets (Model.encode_batch's
     id_off), n_new of them; cached int32 (R): tokens already in the cache;
     free_blocks int32: the blocks to take, in order; table int32 (R, W)."""
+    if stream is not None:
+        kw = dict(slots=slots, positions=positions, lengths=lengths, used=used,
+                  workspace=workspace, status=status)
+        return _on(stream, block_tables, (new_off, cached, free_blocks, table, *kw.values()),
+                   new_off, n_new, cached, free_blocks, table, block_size, **kw)
     op = _flat(new_off, torch.int64, "new_off")
     cp = _flat(cached, torch.int32, "cached")
     fp = _flat(free_blocks, torch.int32, "free_blocks")
@@ -343,27 +357,27 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
     block_size = _int32(block_size, 1, "block_size")
     if n_new < 0:
         raise ValueError(f"n_new: {n_new} is out of range")
-    call = _Call("block_tables", (new_off, cached, free_blocks, table, slots, positions, lengths,
-                                  used, workspace, status), status, stream)
-    try:
-        L = _lib.load()
-        if slots is None:
-            slots = call.empty(n_new, torch.int64)
-        if positions is None:
-            positions = call.empty(n_new, torch.int32)
-        if lengths is None:
-            lengths = call.empty(R, torch.int32)
-        if used is None:
-            used = call.empty(1, torch.int64)
-        if workspace is None:
-            workspace = call.empty(max(L.bpe_block_tables_workspace_bytes(R), 1), torch.uint8)
-        rc = L.bpe_block_tables(op, R, n_new, cp, fp, free_blocks.numel(), table.data_ptr(),
-                                table.shape[1], ts, block_size, slots.data_ptr(),
-                                positions.data_ptr(), lengths.data_ptr(), used.data_ptr(),
-                                workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(),
-                                call.status.data_ptr(), call.stream.cuda_stream)
-        call.end(rc)
-    finally:
-        call.leave()
+    dev = _device("block_tables", new_off, cached, free_blocks, table, slots, positions, lengths,
+                  used, workspace, status)
+    L = _lib.load()
+    st = _status(status, dev)
+    if slots is None:
+        slots = torch.empty(n_new, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(n_new, dtype=torch.int32, device=dev)
+    if lengths is None:
+        lengths = torch.empty(R, dtype=torch.int32, device=dev)
+    if used is None:
+        used = torch.empty(1, dtype=torch.int64, device=dev)
+    if workspace is None:
+        w_bytes = L.bpe_block_tables_workspace_bytes(R)
+        workspace = torch.empty(w_bytes, dtype=torch.uint8, device=dev) if w_bytes else None
+    else:
+        w_bytes = workspace.numel() * workspace.element_size()
+    rc = L.bpe_block_tables(op, R, n_new, cp, fp, free_blocks.numel(), table.data_ptr(),
+                            table.shape[1], ts, block_size, slots.data_ptr(), positions.data_ptr(),
+                            lengths.data_ptr(), used.data_ptr(),
+                            None if workspace is None else workspace.data_ptr(), w_bytes,
+                            st.data_ptr(), _stream(dev))
+    _end("bpe_block_tables", rc, st if status is None else None)
     return slots, positions, lengths, used

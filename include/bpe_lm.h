@@ -146,7 +146,8 @@ typedef struct {
 
 int bpe_process_logits(const bpe_logits_args *args, void *hip_stream);
 
-/* Workspace bytes bpe_block_tables needs (0 for n_requests <= 0). */
+/* Workspace bytes bpe_block_tables needs (0 for few requests: d_workspace may
+ * then be NULL). */
 size_t bpe_block_tables_workspace_bytes(int64_t n_requests);
 
 /*

@@ -125,7 +125,7 @@ def blocks_rc(off=P, R=3, T=10, cached=P, free=P, n_free=5, table=P, W=4, stride
 
 @pytest.mark.parametrize("bad", [
     dict(off=None), dict(cached=None), dict(free=None), dict(table=None), dict(slots=None),
-    dict(positions=None), dict(lengths=None), dict(used=None), dict(ws=None), dict(status=None),
+    dict(positions=None), dict(lengths=None), dict(used=None), dict(ws=None, R=5000), dict(status=None),
     dict(R=-1), dict(T=-1), dict(n_free=-1), dict(W=-1), dict(W=1 << 31, stride=1 << 31),
     dict(stride=3), dict(bs=0), dict(bs=-4), dict(R=0), dict(T=1 << 35), dict(R=(1 << 30) + 1),
 ])
@@ -134,8 +134,9 @@ def test_blocks_refuse(bad):
 
 
 def test_blocks_workspace():
-    need = _lib.load().bpe_block_tables_workspace_bytes(3)
-    assert blocks_rc(ws_bytes=need - 1) == _lib.BPE_EWORKSPACE
+    need = _lib.load().bpe_block_tables_workspace_bytes(5000)
+    assert need >= 5000 * 8
+    assert blocks_rc(R=5000, ws_bytes=need - 1) == _lib.BPE_EWORKSPACE
     assert _lib.load().bpe_block_tables_workspace_bytes(0) == 0
 
 
