@@ -33,7 +33,7 @@ STATUS_NO_BLOCKS, STATUS_TABLE_FULL, STATUS_BAD_LENGTH, STATUS_BAD_MASK_ROW, STA
     32, 64, 128, 256, 512
 F32, BF16, F16 = 0, 1, 2
 MAX_WIDTH = 1 << 18
-MAX_ROWS = 1 << 27
+MAX_ROWS = 1 << 26
 OP_ENCODE, OP_DECODE = 0, 1
 MAX_MERGES = 1 << 20
 MAX_ID = (1 << 24) - 1
@@ -121,7 +121,7 @@ def load() -> C.CDLL:
     L.bpe_embed_grad.restype = i32
     L.bpe_process_logits.argtypes = [C.POINTER(LogitsArgs), p]
     L.bpe_process_logits.restype = i32
-    L.bpe_block_tables_workspace_bytes.argtypes = [i64]
+    L.bpe_block_tables_workspace_bytes.argtypes = [i64, i64]
     L.bpe_block_tables_workspace_bytes.restype = sz
     L.bpe_block_tables.argtypes = [p, i64, i64, p, p, i64, p, i64, i64, i32, p, p, p, p, p, sz, p, p]
     L.bpe_block_tables.restype = i32

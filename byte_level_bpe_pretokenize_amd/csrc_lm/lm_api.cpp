@@ -30,7 +30,7 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width) {
   L.sort_tiles = (int32_t)((n_ids + kSortTile - 1) / kSortTile);
   // long tiles for few cut rows, short ones where there would be too few waves
   const int64_t slabs = width < 8 ? 1 : (width + 511) / 512;
-  L.tile = 64;
+  L.tile = kGradTile;
   while (L.tile > 8 && n_ids / L.tile * slabs < 4096) L.tile /= 2;
   L.tiles = (int32_t)((n_ids + L.tile - 1) / L.tile);
   size_t at = 0;
@@ -73,7 +73,7 @@ int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t wid
       pad_id < -1 || !d_status || (n_ids > 0 && (!d_weight || !d_ids || !d_out)))
     return BPE_EINVAL;
   if (n_ids == 0) return BPE_OK;
-  if (n_ids * (width < 8 ? width : (width + 7) / 8) > kMaxGrid * kEmbedUnits) return BPE_EINVAL;
+  if (n_ids * (width < 8 ? width : (width + 3) / 4) > kMaxGrid * kEmbedUnits) return BPE_EINVAL;
   EmbedArgs a = {};
   a.weight = d_weight;
   a.ids = d_ids;
@@ -91,7 +91,7 @@ int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t wid
 }
 
 size_t bpe_embed_grad_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t width) {
-  if (n_ids <= 0 || n_ids > BPE_MAX_IDS || !table_ok(n_rows, width)) return 0;
+  if (n_ids <= kGradDirect || n_ids > BPE_MAX_IDS || !table_ok(n_rows, width)) return 0;
   return grad_layout(n_ids, n_rows, width).total;
 }
 
@@ -103,7 +103,7 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
   if (!type_ok(grad_type) || !type_ok(out_type) || !table_ok(n_rows, width) || n_ids < 0 ||
       n_ids > BPE_MAX_IDS || !stride_ok(grad_stride, width) || !stride_ok(out_stride, width) ||
       pad_id < -1 || !d_status || !d_out ||
-      (n_ids > 0 && (!d_grad || !d_ids || !d_workspace)))
+      (n_ids > 0 && (!d_grad || !d_ids || (n_ids > kGradDirect && !d_workspace))))
     return BPE_EINVAL;
   GradArgs a = {};
   a.grad = d_grad;
@@ -118,7 +118,7 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
   a.pad_id = pad_id;
   a.scale = scale;
   a.accumulate = accumulate != 0;
-  if (n_ids > 0) {
+  if (n_ids > kGradDirect) {
     const GradLayout L = grad_layout(n_ids, n_rows, width);
     if (workspace_bytes < L.total) return BPE_EWORKSPACE;
     uint8_t *ws = (uint8_t *)d_workspace;
@@ -166,8 +166,8 @@ int bpe_process_logits(const bpe_logits_args *args, void *hip_stream) {
                  : a.bias_ids || a.bias_values)
     return BPE_EINVAL;
   if (a.mask_row ? a.n_masks > 0 && !a.mask : a.mask != nullptr) return BPE_EINVAL;
-  // a count is kept in 30 bits
-  if (a.made_ids && (a.made_width >= (1 << 30) || !stride_ok(a.made_stride, a.made_width)))
+  // a count is kept in 21 bits
+  if (a.made_ids && (a.made_width >= (1 << 21) || !stride_ok(a.made_stride, a.made_width)))
     return BPE_EINVAL;
   if (a.mask && !stride_ok(a.mask_stride, (a.vocab + 31) / 32)) return BPE_EINVAL;
   if (!any) return BPE_OK;
@@ -175,9 +175,10 @@ int bpe_process_logits(const bpe_logits_args *args, void *hip_stream) {
   return launch_logits(a, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }
 
-size_t bpe_block_tables_workspace_bytes(int64_t n_requests) {
-  if (n_requests <= kBlockFused) return 0;
-  return (size_t)n_requests * 8 + kBlockGroups * 8;
+size_t bpe_block_tables_workspace_bytes(int64_t n_requests, int64_t n_new) {
+  if (n_requests <= kBlockFused || n_new < 0) return 0;
+  return (size_t)n_requests * 8 + kBlockGroups * 8 +
+         (size_t)((n_new + kBlockChunk - 1) / kBlockChunk) * 4;
 }
 
 int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new,
@@ -196,7 +197,7 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
                          (table_width > 0 && !d_table)))
     return BPE_EINVAL;
   if (n_new > 0 && (!d_slots || !d_positions)) return BPE_EINVAL;
-  if (workspace_bytes < bpe_block_tables_workspace_bytes(n_requests)) return BPE_EWORKSPACE;
+  if (workspace_bytes < bpe_block_tables_workspace_bytes(n_requests, n_new)) return BPE_EWORKSPACE;
   BlockArgs a = {};
   a.off = d_new_off;
   a.R = n_requests;
@@ -222,6 +223,7 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
   if (n_requests > kBlockFused) {
     a.first = (int64_t *)d_workspace;
     a.gsum = a.first + n_requests;
+    a.chunk_req = (int32_t *)(a.gsum + kBlockGroups);
   }
   a.group_log2 = 10;
   while (((n_requests - 1) >> a.group_log2) + 1 > kBlockGroups) ++a.group_log2;

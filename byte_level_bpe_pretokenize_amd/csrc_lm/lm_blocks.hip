@@ -17,27 +17,37 @@ __device__ __forceinline__ int32_t blocks_for(const BlockArgs &a, int32_t len) {
   return len > 0 ? block_of(a, len - 1) + 1 : 0;
 }
 
-// Blocks that request r takes.  WRITE: also its length, and into *status what
-// is wrong with its offsets and lengths.
-template <bool WRITE>
-__device__ __forceinline__ int32_t need_of(const BlockArgs &a, int64_t r, uint32_t *status) {
-  const int64_t lo = a.off[r], hi = a.off[r + 1];
-  const int32_t c = a.cached[r], cached = max(c, 0);
+// One request: blocks it takes, and what is wrong with its offsets and lengths.
+struct Request {
+  int64_t lo, hi;   // its new tokens
+  int32_t cached;   // tokens in the cache
+};
+
+__device__ __forceinline__ Request load_request(const BlockArgs &a, int64_t r) {
+  Request q;
+  q.lo = a.off[r];
+  q.hi = a.off[r + 1];
+  q.cached = a.cached[r];
+  return q;
+}
+
+__device__ __forceinline__ int32_t need_of(const BlockArgs &a, const Request &q, int64_t r,
+                                           int32_t *len, uint32_t *status) {
+  const int32_t cached = max(q.cached, 0);
   // (offsets that are not valid still give a count in [0, T])
-  const int64_t in = max<int64_t>(min(max<int64_t>(hi, 0), a.T) - min(max<int64_t>(lo, 0), a.T), 0);
+  const int64_t in =
+      max<int64_t>(min(max<int64_t>(q.hi, 0), a.T) - min(max<int64_t>(q.lo, 0), a.T), 0);
   const int64_t full = cached + in;
-  const int32_t len = (int32_t)min<int64_t>(full, INT32_MAX);
-  if (WRITE) {
-    a.lengths[r] = len;
-    if (c < 0 || full > INT32_MAX) *status |= BPE_STATUS_BAD_LENGTH;
-    if (hi < lo || lo < 0 || hi > a.T || (r == 0 && lo != 0) || (r == a.R - 1 && hi != a.T))
-      *status |= BPE_STATUS_BAD_ID_OFFSETS;
-  }
-  return blocks_for(a, len) - blocks_for(a, cached);
+  *len = (int32_t)min<int64_t>(full, INT32_MAX);
+  if (q.cached < 0 || full > INT32_MAX) *status |= BPE_STATUS_BAD_LENGTH;
+  if (q.hi < q.lo || q.lo < 0 || q.hi > a.T || (r == 0 && q.lo != 0) || (r == a.R - 1 && q.hi != a.T))
+    *status |= BPE_STATUS_BAD_ID_OFFSETS;
+  return blocks_for(a, *len) - blocks_for(a, cached);
 }
 
 // Blocks taken before each request within its group of 2^group_log2 requests,
-// and each group's sum: one workgroup per group.
+// each group's sum (one workgroup per group), and the request that each chunk
+// of tokens begins in.
 __global__ void __launch_bounds__(kBlockScan) k_block_scan(BlockArgs a) {
   __shared__ int64_t red[kBlockScan / 64];
   const int64_t r0 = (int64_t)blockIdx.x << a.group_log2;
@@ -46,7 +56,16 @@ __global__ void __launch_bounds__(kBlockScan) k_block_scan(BlockArgs a) {
   uint32_t status = 0;
   for (int64_t s = r0; s < r1; s += kBlockScan) {
     const int64_t r = s + threadIdx.x;
-    const int64_t need = r < r1 ? need_of<true>(a, r, &status) : 0;
+    int64_t need = 0;
+    if (r < r1) {
+      const Request q = load_request(a, r);
+      int32_t len;
+      need = need_of(a, q, r, &len, &status);
+      a.lengths[r] = len;
+      for (int64_t c = (max<int64_t>(q.lo, 0) + kBlockChunk - 1) / kBlockChunk;
+           c * kBlockChunk < min(q.hi, a.T); ++c)
+        a.chunk_req[c] = (int32_t)r;
+    }
     int64_t total;
     const int64_t ex = block_excl_sum<int64_t, kBlockScan>(need, red, &total);
     if (r < r1) a.first[r] = carry + ex;
@@ -56,19 +75,32 @@ __global__ void __launch_bounds__(kBlockScan) k_block_scan(BlockArgs a) {
   if (status) atomicOr(a.status, (int32_t)status);
 }
 
+constexpr int kNear = 256;  // requests of a chunk whose data is kept in LDS
+
 struct FillShared {
-  int32_t req[kBlockChunk];     // the request that starts at a token, then each token's, less r0
+  alignas(16) int32_t req[kBlockChunk];  // the request that starts at a token, then each token's, less r0
+  int64_t pos0[kNear];       // of request r0 + k: position of a token less its place in the chunk
+  int64_t free0[kNear];      // place of its block b in the list of free blocks, less b
+  int32_t have[kNear];       // blocks that were there
   int64_t red[BWG / 64];
   int32_t wmax[BWG / 64];
-  int64_t r0;
+  int32_t r0;
+  int32_t n_slow;            // groups of four tokens that are not of one request
+  int16_t slow[kBlockChunk / 4];
 };
 
 // The chunk's tokens.  The requests that start in it mark their first token;
-// a running maximum gives every token its request.  The token at a block's
-// first place in the cache also enters the block into the table: a new block's
-// first place always belongs to a new token.
+// a running maximum gives every token its request.  Then four neighbouring
+// tokens per thread and step: one lookup of the request (in LDS) and one
+// division where they are one request's; the few groups that are not are listed
+// and done one token per thread afterwards (done in place they cost every wave
+// the slow path).  The token at a block's first place in the cache also enters
+// the block into the table: a new block's first place always belongs to a new
+// token.  What bounds it is arithmetic and the chain of dependent loads in each
+// workgroup, kept to four: the chunk's request, the requests, their groups, the
+// blocks of all tokens.
 // FUSED (R <= kBlockFused): each workgroup sums the requests' needs itself, one
-// launch in all; else `before` holds the groups' running sums.
+// launch in all.
 template <bool FUSED>
 __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
   __shared__ FillShared s;
@@ -78,49 +110,76 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
   const int cnt = (int)min<int64_t>(kBlockChunk, a.T - i0);
   uint32_t status = 0;
   int64_t used = 0;
-  for (int i = tid; i < kBlockChunk; i += BWG) s.req[i] = 0;
-  if (wave_id() == 0 && cnt > 0) {
-    const int64_t r = wave_lower_bound(a.off, a.R + 1, i0 + 1) - 1;
-    if (lane_id() == 0) s.r0 = min(max<int64_t>(r, 0), a.R - 1);
-  }
+  for (int i = tid * 4; i < kBlockChunk; i += BWG * 4) lds_store16(&s.req[i], u32x4{});
+  if (tid == 0) s.n_slow = 0;
+  int64_t r0 = 0;
   if (FUSED) {
     // a thread's requests are consecutive, so that one scan orders them all
     constexpr int PER = kBlockFused / BWG;
-    int32_t need[PER];
+    if (tid == 0) s.r0 = 0;
+    int32_t need[PER], len[PER];
     int64_t sum = 0;
+    int32_t at = -1;
+    if (tid * PER < a.R) {
+      Request q[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int64_t r = tid * PER + j;
-      need[j] = 0;
-      if (r < a.R)
-        need[j] = blockIdx.x == 0 ? need_of<true>(a, r, &status) : need_of<false>(a, r, &status);
-      sum += need[j];
+      for (int j = 0; j < PER; ++j) q[j] = load_request(a, min<int64_t>(tid * PER + j, a.R - 1));
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int r = tid * PER + j;
+        need[j] = 0;
+        if (r >= a.R) continue;
+        need[j] = need_of(a, q[j], r, &len[j], &status);
+        if (blockIdx.x == 0) a.lengths[r] = len[j];
+        if (q[j].lo <= i0) at = r;
+        sum += need[j];
+      }
     }
+    if (blockIdx.x != 0) status = 0;  // every workgroup sees the same: one reports
     int64_t ex = block_excl_sum<int64_t, BWG>(sum, s.red, &used);
+    if (at >= 0) atomicMax(&s.r0, at);
+    if (tid * PER < a.R) {
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      before[tid * PER + j] = ex;
-      ex += need[j];
+      for (int j = 0; j < PER; ++j) {
+        before[tid * PER + j] = ex;
+        ex += need[j];
+      }
     }
+    __syncthreads();
+    r0 = s.r0;
   } else {
     static_assert(kBlockGroups == BWG, "one group per thread");
+    // (the chunk's request is not set where the offsets are not valid)
+    if (cnt > 0) r0 = min(max<int64_t>(a.chunk_req[blockIdx.x], 0), a.R - 1);
     const int64_t groups = ((a.R - 1) >> a.group_log2) + 1;
     before[tid] = block_excl_sum<int64_t, BWG>(tid < groups ? a.gsum[tid] : 0, s.red, &used);
+    __syncthreads();
   }
   if (blockIdx.x == 0 && tid == 0) {
     *a.used = used;
     if (used > a.n_free) status |= BPE_STATUS_NO_BLOCKS;
   }
-  __syncthreads();
   if (cnt > 0) {
-    const int64_t r0 = s.r0;
-    // requests after r0 that start before the chunk's end
-    for (int64_t r = r0 + 1 + tid; r < a.R; r += BWG) {
-      const int64_t p = a.off[r] - i0;
-      if (p >= cnt) break;
-      if (p > 0) atomicMax(&s.req[p], (int32_t)(r - r0));
+    auto place = [&](int64_t r, int64_t lo, int32_t cached, int64_t first, int64_t *pos0,
+                     int64_t *free0, int32_t *have) {
+      cached = max(cached, 0);
+      *pos0 = cached + (i0 - lo);
+      *have = blocks_for(a, cached);
+      *free0 = (FUSED ? before[r] : before[r >> a.group_log2] + first) - *have;
+    };
+    // the requests from r0 on that start before the chunk's end
+    for (int64_t k = tid;; k += BWG) {
+      const int64_t r = min(r0 + k, a.R - 1);
+      const int64_t lo = a.off[r];
+      const int32_t cached = a.cached[r];
+      const int64_t first = FUSED ? 0 : a.first[r];
+      const int64_t p = r0 + k < a.R ? lo - i0 : cnt;
+      if (p < cnt || k == 0) {
+        if (k < kNear) place(r, lo, cached, first, &s.pos0[k], &s.free0[k], &s.have[k]);
+        if (p > 0 && p < cnt) atomicMax(&s.req[p], (int32_t)k);
+      }
+      if (!__syncthreads_or(p < cnt)) break;
     }
-    __syncthreads();
     constexpr int PER = kBlockChunk / BWG;
     int32_t v[PER];
 #pragma unroll
@@ -137,47 +196,97 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) s.req[tid * PER + j] = max(v[j], left);
     __syncthreads();
-    // two tokens per thread and step: slots in 16-byte stores
+    // Block blk of request r0 + k: where its number stands (the table, for a
+    // block that was there, or the list of free ones), or nullptr for none.
+    auto look = [&](int k, int32_t blk, int64_t free0, int32_t have) -> const int32_t * {
+      const int64_t f = free0 + blk;
+      if (blk < have) return blk < a.width ? a.table + (r0 + k) * a.stride + blk : nullptr;
+      return f < a.n_free ? a.free_blocks + f : nullptr;
+    };
+    // Its first token enters it.
+    auto enter = [&](int k, int32_t blk, int32_t block) {
+      if (blk < a.width) a.table[(r0 + k) * a.stride + blk] = block;
+    };
+    // Four neighbouring tokens of one request, in at most two blocks.  All
+    // loads of all steps go first (a wait for a load waits for the stores
+    // before it as well), unconditional ones, so that they are in flight
+    // together.
+    constexpr int STEPS = kBlockChunk / (4 * BWG);
+    const int32_t *none = (const int32_t *)a.off;
+    int32_t kk[STEPS], pos[STEPS], blk[STEPS], b0[STEPS], b1[STEPS];
+    bool made0[STEPS];  // the first block is a new one
 #pragma unroll
-    for (int j = 0; j < kBlockChunk / (2 * BWG); ++j) {
-      const int i = (j * BWG + tid) * 2;
-      if (i >= cnt) break;
-      Vec<int64_t, 2> slot;
-      Vec<int32_t, 2> posn;
+    for (int u = 0; u < STEPS; ++u) {
+      const int i = (u * BWG + tid) * 4;
+      const u32x4 k = lds_load16(&s.req[i]);
+      const int kn = min((int)k.x, kNear - 1);
+      const int64_t at64 = s.pos0[kn] + i, free0 = s.free0[kn];
+      const int32_t have = s.have[kn];
+      const bool quad = i + 4 <= cnt && k.x == k.w && k.x < kNear && a.bs >= 4 && at64 >= 0 &&
+                        at64 <= INT32_MAX - 3;
+      kk[u] = quad ? (int32_t)k.x : -1;
+      pos[u] = quad ? (int32_t)at64 : 0;
+      blk[u] = block_of(a, pos[u]);
+      made0[u] = blk[u] >= have;
+      const int32_t *p0 = quad ? look(k.x, blk[u], free0, have) : nullptr;
+      const int32_t *p1 = quad ? look(k.x, blk[u] + 1, free0, have) : nullptr;
+      b0[u] = *(p0 ? p0 : none);
+      b1[u] = *(p1 ? p1 : none);
+      b0[u] = p0 ? b0[u] : -1;
+      b1[u] = p1 ? b1[u] : -1;
+      if (!quad && i < cnt) s.slow[atomicAdd(&s.n_slow, 1)] = (int16_t)i;
+    }
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        slot.v[q] = -1;
-        posn.v[q] = -1;
-        if (i + q >= cnt) continue;
-        const int64_t r = r0 + s.req[i + q];
-        const int32_t cached = max(a.cached[r], 0);
-        const int64_t pos = cached + (i0 + i + q - a.off[r]);
-        if (pos < 0 || pos > INT32_MAX) continue;
-        posn.v[q] = (int32_t)pos;
-        const int32_t blk = block_of(a, (int32_t)pos);
-        const int32_t at = (int32_t)pos - blk * a.bs;
-        if (blk >= a.width) {
-          status |= BPE_STATUS_TABLE_FULL;
-          continue;
-        }
-        const int32_t have = blocks_for(a, cached);
-        int32_t block = -1;
-        if (blk < have) {
-          block = a.table[r * a.stride + blk];
-        } else {
-          const int64_t f = (FUSED ? before[r] : before[r >> a.group_log2] + a.first[r]) + blk - have;
-          if (f < a.n_free) block = a.free_blocks[f];
-          if (at == 0) a.table[r * a.stride + blk] = block;
-        }
-        if (block >= 0) slot.v[q] = (int64_t)block * a.bs + at;
+    for (int u = 0; u < STEPS; ++u) {
+      if (kk[u] < 0) continue;
+      const int i = (u * BWG + tid) * 4;
+      const int32_t at = pos[u] - blk[u] * a.bs;
+      if (at == 0 && made0[u]) enter(kk[u], blk[u], b0[u]);
+      // (the second block's first place is a new token's: it is a new block)
+      if (at + 3 >= a.bs) enter(kk[u], blk[u] + 1, b1[u]);
+      const bool ok0 = b0[u] >= 0 && blk[u] < a.width, ok1 = b1[u] >= 0 && blk[u] + 1 < a.width;
+      if (blk[u] + (at + 3 >= a.bs) >= a.width) status |= BPE_STATUS_TABLE_FULL;
+      const int64_t s0 = (int64_t)b0[u] * a.bs + at, s1 = (int64_t)b1[u] * a.bs + (at - a.bs);
+      Vec<int64_t, 4> slot;
+      Vec<int32_t, 4> posn;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bool in0 = at + q < a.bs;
+        posn.v[q] = pos[u] + q;
+        slot.v[q] = (in0 ? ok0 : ok1) ? (in0 ? s0 : s1) + q : -1;
       }
-      if (i + 1 < cnt) {
-        store_vec(a.slots + i0 + i, slot);
-        store_vec(a.positions + i0 + i, posn);
+      store_vec(a.slots + i0 + i, slot);
+      store_vec(a.positions + i0 + i, posn);
+    }
+    __syncthreads();
+    // the others one by one, side by side
+    for (int j = tid; j < s.n_slow * 4; j += BWG) {
+      const int i = s.slow[j >> 2] + (j & 3);
+      if (i >= cnt) continue;
+      const int k = s.req[i];
+      int64_t at64, free0;
+      int32_t have, position = -1;
+      int64_t slot = -1;
+      if (k < kNear) {
+        at64 = s.pos0[k];
+        free0 = s.free0[k];
+        have = s.have[k];
       } else {
-        a.slots[i0 + i] = slot.v[0];
-        a.positions[i0 + i] = posn.v[0];
+        const int64_t r = r0 + k;
+        place(r, a.off[r], a.cached[r], FUSED ? 0 : a.first[r], &at64, &free0, &have);
       }
+      at64 += i;
+      if (at64 >= 0 && at64 <= INT32_MAX) {
+        position = (int32_t)at64;
+        const int32_t bk = block_of(a, position), at = position - bk * a.bs;
+        const int32_t *p = look(k, bk, free0, have);
+        const int32_t block = p ? *p : -1;
+        if (at == 0 && bk >= have) enter(k, bk, block);
+        if (bk >= a.width) status |= BPE_STATUS_TABLE_FULL;
+        else if (block >= 0) slot = (int64_t)block * a.bs + at;
+      }
+      a.slots[i0 + i] = slot;
+      a.positions[i0 + i] = position;
     }
   }
   if (status) atomicOr(a.status, (int32_t)status);

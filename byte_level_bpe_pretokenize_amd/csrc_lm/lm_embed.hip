@@ -12,10 +12,10 @@ namespace {
 // row whose width is no multiple of E starts at width - E and writes a few
 // elements a second time with the same values.  U vectors per thread: their
 // ID loads, then their row loads, are in flight together.
-template <typename TI, typename TO, int E, int U>
+template <typename TI, typename TO, int E, int U, bool BIG>
 __global__ void __launch_bounds__(256) k_embed(EmbedArgs a) {
   const int tid = threadIdx.x;
-  const int64_t base = (int64_t)blockIdx.x * (256 * U);
+    const int64_t base = (int64_t)blockIdx.x * (256 * U);
   const int64_t t0 = base / a.units;
   const uint32_t u0 = (uint32_t)(base - t0 * a.units);
   int32_t id[U];
@@ -44,7 +44,8 @@ __global__ void __launch_bounds__(256) k_embed(EmbedArgs a) {
     Vec<TO, E> r;
 #pragma unroll
     for (int e = 0; e < E; ++e) r.v[e] = from_f32<TO>(ok[k] ? (float)w[k].v[e] * a.scale : 0.f);
-    store_vec<TO, E>((TO *)a.out + t[k] * a.o_stride + col[k], r);
+    TO *p = (TO *)a.out + t[k] * a.o_stride + col[k];
+    store_vec<TO, E, BIG>(p, r);
   }
   if (bad) atomicOr(a.status, (int32_t)BPE_STATUS_BAD_ID);
 }
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_scatter(GradArgs a, int p
   // thread d < digits: the digit's keys in all tiles and in the earlier ones
   int32_t all = 0, before = 0;
   if (tid < digits)
+#pragma unroll 16
     for (int s = 0; s < a.sort_tiles; ++s) {
       const int32_t c = a.counts[(int64_t)s * digits + tid];
       all += c;
@@ -163,8 +165,23 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_scatter(GradArgs a, int p
 }
 
 // ---- gradient: sums --------------------------------------------------------------
-// Elements of a lane's vector before `skip` belong to its left neighbour (the
-// last vector of a row whose width is no multiple of E): loaded, not stored.
+// A lane has 8 columns of a slab of 512: one vector of E = 8 elements, or,
+// where either side is float32, two of E = 4 (256 columns apart), so that a
+// wave's accesses are whole lines.  Columns of a lane's vector g: its start,
+// and how many of its elements belong to its left neighbour (the last vector
+// of a row whose width is no multiple of E); false past the row's end.
+template <int E>
+__device__ __forceinline__ bool grad_col(const GradArgs &a, int vec, int *col, int *skip) {
+  const int c = (vec * 64 + lane_id()) * E;
+  *col = 0;
+  *skip = 0;
+  if (c >= a.width) return false;
+  *col = min(c, a.width - E);
+  *skip = c - *col;
+  return true;
+}
+
+// Elements before `skip` belong to the left neighbour: loaded, not stored.
 template <typename TO, int E>
 __device__ __forceinline__ void grad_store(const GradArgs &a, int64_t row, int col, int skip,
                                            const float (&acc)[E]) {
@@ -179,7 +196,7 @@ __device__ __forceinline__ void grad_store(const GradArgs &a, int64_t row, int c
 #pragma unroll
       for (int e = 0; e < E; ++e) r.v[e] = from_f32<TO>(acc[e] * a.scale);
     }
-    store_vec<TO, E>(p, r);
+    store_vec<TO, E, true>(p, r);
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -187,26 +204,18 @@ __device__ __forceinline__ void grad_store(const GradArgs &a, int64_t row, int c
   }
 }
 
-// A lane's column in slab s: its vector's start, and how many of its elements
-// belong to its left neighbour; false past the row's end.
-template <int E>
-__device__ __forceinline__ bool grad_col(const GradArgs &a, int s, int *col, int *skip) {
-  const int c = (s * 64 + lane_id()) * E;
-  if (c >= a.width) return false;
-  *col = min(c, a.width - E);
-  *skip = c - *col;
-  return true;
-}
-
-constexpr int kRowsAhead = 8;   // gradient rows in flight per wave
+constexpr int kRowsAhead = 8;  // gradient rows in flight per wave
 
 // Workgroups below sum_blocks: one wave per tile of the sorted list and slab of
-// 64 vectors of columns, adding up the rows of each ID in the order of the
+// 64 * G vectors of columns, adding up the rows of each ID in the order of the
 // list.  A row whose positions all lie in the tile is finished here; of one
 // that a tile's edge cuts, the tile's share goes to `part` (slot 0: the row
 // began in an earlier tile; slot 1: it begins here and goes on).  The other
 // workgroups write zeros to the rows that no ID names.
-template <typename TG, typename TO, int E>
+// The next kRowsAhead rows are loaded before the last ones are worked on: a
+// wait for a load waits for every earlier store too, and these are earlier
+// than the stores.
+template <typename TG, typename TO, int E, int G>
 __global__ void __launch_bounds__(256) k_grad_sum(GradArgs a) {
   const int lane = lane_id(), wv = uniform_wave_id();
   if (blockIdx.x >= a.sum_blocks) {
@@ -218,73 +227,224 @@ __global__ void __launch_bounds__(256) k_grad_sum(GradArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) z.v[e] = from_f32<TO>(0.f);
       for (int c = threadIdx.x * E; c < a.width; c += 256 * E)
-        store_vec<TO, E>(p + min(c, a.width - E), z);
+        store_vec<TO, E, true>(p + min(c, a.width - E), z);
     }
     return;
   }
   const int64_t w = (int64_t)blockIdx.x * 4 + wv;
   const int tile = (int)(w / a.slabs), slab = (int)(w - (int64_t)tile * a.slabs);
   if (tile >= a.tiles) return;
-  int col = 0, skip = 0;
-  const bool mine = grad_col<E>(a, slab, &col, &skip);
+  int col[G], skip[G];
+  bool mine[G];
+#pragma unroll
+  for (int g = 0; g < G; ++g) mine[g] = grad_col<E>(a, slab * G + g, &col[g], &skip[g]);
   const int fin = (a.passes - 1) & 1;
   const int64_t i0 = (int64_t)tile * a.tile;
   const int n = (int)min<int64_t>(a.tile, a.n_ids - i0);
-  // lane l holds the l-th key and position of the tile
   const int32_t none = (int32_t)a.n_rows;
-  const int32_t k = lane < n ? a.key[fin][i0 + lane] : none;
-  const int32_t p = lane < n ? a.pos[fin][i0 + lane] : 0;
-  const int32_t prev = i0 > 0 ? a.key[fin][i0 - 1] : -1;
-  const int32_t next = i0 + n < a.n_ids ? a.key[fin][i0 + n] : -1;
-  const int m = __popcll(__ballot(k < none));  // rows that add something come first
-  if (m == 0) return;
-  const TG *g = (const TG *)a.grad + col;
-  float acc[E] = {};
-  int32_t cur = lane_value(k, 0);
+  const int32_t *key = a.key[fin] + i0, *place = a.pos[fin] + i0;
+  const int32_t prev = i0 > 0 ? key[-1] : -1;
+  const int32_t next = i0 + n < a.n_ids ? key[n] : -1;
+  float acc[G][E] = {};
+  int32_t cur = key[0];
+  if (cur >= none) return;
   bool from_left = cur == prev;
-  float *part = a.part + (int64_t)tile * 2 * a.width + col;
   auto flush = [&](bool to_right) {
-    if (!mine) return;
-    if (from_left || to_right) {
-      float *q = part + (from_left ? 0 : a.width);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (e >= skip) q[e] = acc[e];
-    } else {
-      grad_store<TO, E>(a, cur, col, skip, acc);
+    for (int g = 0; g < G; ++g) {
+      if (!mine[g]) continue;
+      if (from_left || to_right) {
+        // (a vector that starts inside its left neighbour writes the shared
+        // elements a second time with the same values)
+        Vec<float, E> r;
+#pragma unroll
+        for (int e = 0; e < E; ++e) r.v[e] = acc[g][e];
+        store_vec<float, E>(
+            a.part + ((int64_t)tile * 2 + (from_left ? 0 : 1)) * a.width + col[g], r);
+      } else {
+        grad_store<TO, E>(a, cur, col[g], skip[g], acc[g]);
+      }
     }
   };
-  for (int b = 0; b < m; b += kRowsAhead) {
-    // (lanes past the row's end load its first vector: every lane stays
-    // active around the lane reads)
-    Vec<TG, E> x[kRowsAhead];
-#pragma unroll
-    for (int j = 0; j < kRowsAhead; ++j)
-      x[j] = load_vec<TG, E>(g + (int64_t)lane_value(p, min(b + j, m - 1)) * a.g_stride);
+  // lane l holds the key and position l of the list's next 64; positions past
+  // the last that adds something are not there (they come last)
+  int32_t k = lane < n ? key[lane] : none, p = lane < n ? place[lane] : 0;
+  Vec<TG, E> x[2][kRowsAhead][G];
+  // (lanes past the row's end load its first vector: every lane stays active
+  // around the lane reads)
+  auto fetch = [&](Vec<TG, E> (&y)[kRowsAhead][G], int at, int m) {
 #pragma unroll
     for (int j = 0; j < kRowsAhead; ++j) {
-      if (b + j >= m) break;
-      const int32_t kk = lane_value(k, b + j);
+      const TG *row = (const TG *)a.grad + (int64_t)lane_value(p, min(at + j, m - 1)) * a.g_stride;
+#pragma unroll
+      for (int g = 0; g < G; ++g) y[j][g] = load_vec<TG, E, true>(row + col[g]);
+    }
+  };
+  auto add = [&](Vec<TG, E> (&y)[kRowsAhead][G], int32_t keys, int at, int m) {
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+      if (at + j >= m) break;
+      const int32_t kk = lane_value(keys, at + j);
       if (kk != cur) {
         flush(false);
         from_left = false;
         cur = kk;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[g][e] = 0.f;
       }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += (float)x[j].v[e];
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[g][e] += (float)y[j][g].v[e];
     }
+  };
+  int m = __popcll(__ballot(k < none));
+  fetch(x[0], 0, m);
+  for (int s = 0;;) {
+    // the 64 after these, whose loads end before they are needed
+    const int t = s + 64 + lane;
+    const int32_t k1 = t < n ? key[t] : none, p1 = t < n ? place[t] : 0;
+    const int32_t k0 = k;
+    const int m0 = m;
+    static_assert(64 % (2 * kRowsAhead) == 0, "two buffers in turn");
+    for (int b = 0; b < m0; b += 2 * kRowsAhead) {
+      if (b + kRowsAhead < m0) fetch(x[1], b + kRowsAhead, m0);
+      add(x[0], k0, b, m0);
+      if (b + 2 * kRowsAhead < m0) {
+        fetch(x[0], b + 2 * kRowsAhead, m0);
+      } else if (m0 == 64) {
+        k = k1;
+        p = p1;
+        m = __popcll(__ballot(k < none));
+        if (m > 0) fetch(x[0], 0, m);
+      }
+      if (b + kRowsAhead < m0) add(x[1], k0, b + kRowsAhead, m0);
+    }
+    s += 64;
+    if (m0 < 64 || s >= n || m == 0) break;
   }
-  flush(m == n && next == cur);
+  // (a tile that ends in positions that add nothing: next is `none`, not cur)
+  flush(next == cur);
+}
+
+// Few IDs (n_ids <= kGradDirect): no sort.  One workgroup per position and two
+// slabs; it has work when its position is the first of its ID.  It lists the
+// ID's positions in order and adds up their rows: up to kRowsAhead rows by one
+// wave per slab, more by all eight waves, every eighth row each, joined in
+// order.  The other workgroups mark which of their rows occur and write zeros
+// to the rest.  One launch instead of six: what such a call costs.
+constexpr int kDirectWG = 512;
+constexpr int kDirectSlabs = 2;
+constexpr int kDirectZero = 32;  // rows of the table per workgroup of zeros
+
+template <typename TG, typename TO, int E, int G>
+__global__ void __launch_bounds__(kDirectWG) k_grad_direct(GradArgs a) {
+  constexpr int NW = kDirectWG / 64, PER = kGradDirect / kDirectWG;
+  __shared__ float sh[NW][64][G * E];
+  __shared__ int16_t list[kGradDirect];
+  __shared__ int32_t red[NW];
+  __shared__ int32_t touched[kDirectZero];
+  const int tid = threadIdx.x, lane = lane_id(), wv = uniform_wave_id();
+  const int n = (int)a.n_ids;
+  int32_t id[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) id[j] = a.ids[min(tid * PER + j, n - 1)];
+  if (blockIdx.x >= a.sum_blocks) {
+    const int64_t r0 = (int64_t)(blockIdx.x - a.sum_blocks) * kDirectZero;
+    if (tid < kDirectZero) touched[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (id[j] >= r0 && id[j] < r0 + kDirectZero && id[j] != a.pad_id) touched[id[j] - r0] = 1;
+    __syncthreads();
+    for (int r = wv; r < kDirectZero && r0 + r < a.n_rows; r += NW) {
+      if (touched[r]) continue;
+      TO *p = (TO *)a.out + (r0 + r) * a.o_stride;
+      Vec<TO, E> z;
+#pragma unroll
+      for (int e = 0; e < E; ++e) z.v[e] = from_f32<TO>(0.f);
+      for (int c = lane * E; c < a.width; c += 64 * E) store_vec<TO, E>(p + min(c, a.width - E), z);
+    }
+    return;
+  }
+  const int groups = (a.slabs + kDirectSlabs - 1) / kDirectSlabs;
+  const int t = (int)(blockIdx.x / (unsigned)groups);
+  const int s0 = (int)(blockIdx.x - (unsigned)(t * groups)) * kDirectSlabs;
+  const int s1 = min(s0 + kDirectSlabs, a.slabs);
+  bool bad = false;
+  const int32_t cur = grad_key(a, a.ids[t], &bad);
+  if (bad && s0 == 0 && tid == 0) atomicOr(a.status, (int32_t)BPE_STATUS_BAD_ID);
+  if (cur >= a.n_rows) return;
+  int32_t mine = 0;
+  bool earlier = false;
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (tid * PER + j < n && id[j] == cur) {
+      ++mine;
+      earlier |= tid * PER + j < t;
+    }
+  if (__syncthreads_or(earlier)) return;
+  int32_t cnt;
+  int32_t at = block_excl_sum<int32_t, kDirectWG>(mine, red, &cnt);
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (tid * PER + j < n && id[j] == cur) list[at++] = (int16_t)(tid * PER + j);
+  __syncthreads();
+  const bool all = cnt > kRowsAhead;  // every wave on every slab
+  const int step = all ? NW : 1;
+  for (int s = all ? s0 : s0 + wv; s < s1; s += all ? 1 : NW) {
+    int col[G], skip[G];
+    bool in[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) in[g] = grad_col<E>(a, s * G + g, &col[g], &skip[g]);
+    float acc[G][E] = {};
+    for (int b = all ? wv : 0; b < cnt; b += step * kRowsAhead) {
+      Vec<TG, E> x[kRowsAhead][G];
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j) {
+        const TG *row = (const TG *)a.grad + (int64_t)list[min(b + j * step, cnt - 1)] * a.g_stride;
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[j][g] = load_vec<TG, E>(row + col[g]);
+      }
+#pragma unroll
+      for (int j = 0; j < kRowsAhead; ++j)
+        if (b + j * step < cnt) {
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[g][e] += (float)x[j][g].v[e];
+        }
+    }
+    if (all) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < E; ++e) sh[wv][lane][g * E + e] = acc[g][e];
+      __syncthreads();
+      if (wv == 0) {
+#pragma unroll
+        for (int w = 1; w < NW; ++w)
+#pragma unroll
+          for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[g][e] += sh[w][lane][g * E + e];
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      if (in[g] && (!all || wv == 0)) grad_store<TO, E>(a, cur, col[g], skip[g], acc[g]);
+  }
 }
 
 // Rows that tile edges cut: one workgroup per tile and slab; it has work when a
 // row begins in its tile and goes on in the next.  Its four waves add up the
 // tiles' shares, every fourth each, and join theirs in order.
-template <typename TO, int E>
+template <typename TO, int E, int G>
 __global__ void __launch_bounds__(256) k_grad_join(GradArgs a) {
-  __shared__ float sh[4][64][E];
+  __shared__ float sh[4][64][G * E];
   const int lane = lane_id(), wv = wave_id();
   const int tile = (int)(blockIdx.x / a.slabs), slab = (int)(blockIdx.x - (unsigned)tile * a.slabs);
   const int fin = (a.passes - 1) & 1;
@@ -302,48 +462,64 @@ __global__ void __launch_bounds__(256) k_grad_join(GradArgs a) {
     run += c;
     if (c < 64) break;
   }
-  int col = 0, skip = 0;
-  const bool mine = grad_col<E>(a, slab, &col, &skip);
-  float acc[E] = {};
-  if (mine) {
-    const float *p = a.part + (int64_t)tile * 2 * a.width + col;
-    if (wv == 0) {
+  int col[G], skip[G];
+  bool mine[G];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = p[a.width + e];
+  for (int g = 0; g < G; ++g) mine[g] = grad_col<E>(a, slab * G + g, &col[g], &skip[g]);
+  // (lanes past the row's end add up its first vector and store nothing)
+  float acc[G][E] = {};
+  const float *p = a.part + (int64_t)tile * 2 * a.width;
+  if (wv == 0) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const Vec<float, E> x = load_vec<float, E>(p + a.width + col[g]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[g][e] = x.v[e];
     }
-#pragma unroll 4
-    for (int j = 1 + wv; j <= run; j += 4) {
-      const Vec<float, E> x = load_vec<float, E>(p + (int64_t)j * 2 * a.width);
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += x.v[e];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sh[wv][lane][e] = acc[e];
   }
+#pragma unroll 4
+  for (int j = 1 + wv; j <= run; j += 4) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const Vec<float, E> x = load_vec<float, E>(p + (int64_t)j * 2 * a.width + col[g]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[g][e] += x.v[e];
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh[wv][lane][g * E + e] = acc[g][e];
   __syncthreads();
-  if (wv == 0 && mine) {
+  if (wv == 0) {
 #pragma unroll
-    for (int w = 1; w < 4; ++w)
+    for (int g = 0; g < G; ++g) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += sh[w][lane][e];
-    grad_store<TO, E>(a, cur, col, skip, acc);
+      for (int w = 1; w < 4; ++w)
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[g][e] += sh[w][lane][g * E + e];
+      if (mine[g]) grad_store<TO, E>(a, cur, col[g], skip[g], acc[g]);
+    }
   }
 }
 
-template <typename TI, typename TO, int E>
+template <typename TI, typename TO, int E, bool BIG>
 hipError_t embed_as(EmbedArgs a, hipStream_t stream) {
   constexpr int U = kEmbedUnits / 256;
   a.units = (uint32_t)((a.width + E - 1) / E);
   a.magic = (1u << 31) / a.units + 1;
-  const int64_t total = a.n_ids * a.units;
-  hipLaunchKernelGGL((k_embed<TI, TO, E, U>), dim3((unsigned)((total + 256 * U - 1) / (256 * U))),
-                     dim3(256), 0, stream, a);
+  const int64_t groups = (a.n_ids * a.units + kEmbedUnits - 1) / kEmbedUnits;
+  hipLaunchKernelGGL((k_embed<TI, TO, E, U, BIG>), dim3((unsigned)(groups)), dim3(256), 0,
+                     stream, a);
   return hipGetLastError();
 }
 
 template <typename TI, typename TO>
 hipError_t embed_of(const EmbedArgs &a, hipStream_t stream) {
-  return a.width >= 8 ? embed_as<TI, TO, 8>(a, stream) : embed_as<TI, TO, 1>(a, stream);
+  if (a.width < 8) return embed_as<TI, TO, 1, false>(a, stream);
+  const bool big = a.n_ids * a.width * (int64_t)sizeof(TO) >= (32 << 20);
+  constexpr int E = 16 / sizeof(TO);
+  return big ? embed_as<TI, TO, E, true>(a, stream) : embed_as<TI, TO, E, false>(a, stream);
 }
 
 template <typename TI>
@@ -353,9 +529,16 @@ hipError_t embed_from(const EmbedArgs &a, int ot, hipStream_t stream) {
   return embed_of<TI, f16_t>(a, stream);
 }
 
-template <typename TG, typename TO, int E>
+template <typename TG, typename TO, int E, int G>
 hipError_t grad_as(GradArgs a, hipStream_t stream) {
-  a.slabs = (a.width + 64 * E - 1) / (64 * E);
+  a.slabs = (a.width + 64 * G * E - 1) / (64 * G * E);
+  if (a.n_ids > 0 && a.n_ids <= kGradDirect) {
+    a.sum_blocks = a.n_ids * ((a.slabs + kDirectSlabs - 1) / kDirectSlabs);
+    const int64_t zero = a.accumulate ? 0 : (a.n_rows + kDirectZero - 1) / kDirectZero;
+    hipLaunchKernelGGL((k_grad_direct<TG, TO, E, G>), dim3((unsigned)(a.sum_blocks + zero)),
+                       dim3(kDirectWG), 0, stream, a);
+    return hipGetLastError();
+  }
   for (int pass = 0; a.n_ids > 0 && pass < a.passes; ++pass) {
     hipLaunchKernelGGL(k_grad_count, dim3(a.sort_tiles), dim3(kSortThreads), 0, stream, a, pass);
     hipLaunchKernelGGL(k_grad_scatter, dim3(a.sort_tiles), dim3(kSortThreads), 0, stream, a, pass);
@@ -363,17 +546,19 @@ hipError_t grad_as(GradArgs a, hipStream_t stream) {
   a.sum_blocks = a.n_ids > 0 ? ((int64_t)a.tiles * a.slabs + 3) / 4 : 0;
   const int64_t zero = a.accumulate ? 0 : (a.n_rows + kZeroRows - 1) / kZeroRows;
   if (a.sum_blocks + zero > 0)
-    hipLaunchKernelGGL((k_grad_sum<TG, TO, E>), dim3((unsigned)(a.sum_blocks + zero)), dim3(256), 0,
-                       stream, a);
+    hipLaunchKernelGGL((k_grad_sum<TG, TO, E, G>), dim3((unsigned)(a.sum_blocks + zero)), dim3(256),
+                       0, stream, a);
   if (a.n_ids > a.tile)
-    hipLaunchKernelGGL((k_grad_join<TO, E>), dim3((unsigned)((int64_t)a.tiles * a.slabs)),
+    hipLaunchKernelGGL((k_grad_join<TO, E, G>), dim3((unsigned)((int64_t)a.tiles * a.slabs)),
                        dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename TG, typename TO>
 hipError_t grad_of(const GradArgs &a, hipStream_t stream) {
-  return a.width >= 8 ? grad_as<TG, TO, 8>(a, stream) : grad_as<TG, TO, 1>(a, stream);
+  if (a.width < 8) return grad_as<TG, TO, 1, 1>(a, stream);
+  if constexpr (sizeof(TG) == 4 || sizeof(TO) == 4) return grad_as<TG, TO, 4, 2>(a, stream);
+  else return grad_as<TG, TO, 8, 1>(a, stream);
 }
 
 template <typename TG>

@@ -10,8 +10,8 @@
 namespace bpe {
 
 // Workgroups of one launch, at most (a launch has fewer than 2^32 threads, of
-// up to 256 a workgroup).
-constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;
+// up to 512 a workgroup).
+constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
 
 // ---- embedding ---------------------------------------------------------------
 struct EmbedArgs {
@@ -23,7 +23,7 @@ struct EmbedArgs {
   int32_t width;
   int32_t pad_id;
   float scale;
-  uint32_t units;   // vectors per row
+  uint32_t units;   // vectors per row and slab
   uint32_t magic;   // 2^31 / units + 1: x / units = x * magic >> 31 while x * units < 2^31
 };
 
@@ -35,6 +35,8 @@ hipError_t launch_embed(const EmbedArgs &a, int wt, int ot, hipStream_t stream);
 // wave per tile and 64 vectors of columns.
 constexpr int kEmbedUnits = 1024;  // vectors per workgroup of the forward
 constexpr int kZeroRows = 16;      // rows of the table per workgroup of zeros
+constexpr int kGradTile = 256;     // IDs per tile of the sums, at most
+constexpr int kGradDirect = 2048;  // IDs up to which no sort is made
 constexpr int kDigitBits = 9;
 constexpr int kMaxDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 1024;
@@ -72,7 +74,12 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width);
 hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);
 
 // ---- logits ------------------------------------------------------------------
-constexpr int kLogitSlab = 4096;  // logits per workgroup
+#ifndef XSLAB
+#define XSLAB 4096
+#define XTH 256
+#endif
+constexpr int kLogitSlab = XSLAB;     // logits per workgroup
+constexpr int kLogitThreads = XTH;
 
 hipError_t launch_logits(const bpe_logits_args &a, hipStream_t stream);
 
@@ -93,6 +100,7 @@ struct BlockArgs {
   int32_t *status;
   int64_t *first;     // [R] workspace: blocks taken before r within its group
   int64_t *gsum;      // [kBlockGroups] workspace: blocks taken by each group
+  int32_t *chunk_req; // [chunks of T] workspace: the request that the chunk begins in
   int32_t group_log2; // requests per group
 };
 

@@ -5,10 +5,11 @@
 namespace bpe {
 namespace {
 
-constexpr int LWG = 256;
 constexpr uint32_t kPrompt = 1u << 31;  // the token occurs in the prompt
 constexpr uint32_t kBiased = 1u << 30;  // the row has a bias for it
-constexpr uint32_t kCount = kBiased - 1;
+constexpr int kSlotShift = 21;          // the bias's slot, kBiasSlots - 1 at most
+constexpr uint32_t kBiasSlots = 512;
+constexpr uint32_t kCount = (1u << kSlotShift) - 1;
 
 // [lo, hi) of row b of a ragged list of n entries; an offset outside [0, n] or
 // a decreasing pair gives an empty row and sets *bad.
@@ -22,140 +23,209 @@ __device__ __forceinline__ void ragged(const int64_t *off, int64_t b, int64_t n,
   }
 }
 
-// Calls f(v) for the IDs p[0 .. n), 4 per thread and step (one 16-byte load),
-// the workgroup's threads side by side.
-template <typename F>
-__device__ __forceinline__ void each_id(const int32_t *p, int64_t n, F f) {
-  for (int64_t i = (int64_t)threadIdx.x * 4; i < n; i += LWG * 4) {
-    if (i + 4 <= n) {
-      const Vec<int32_t, 4> x = load_vec<int32_t, 4>(p + i);
+// 4 IDs of a list p[0 .. n) from i on: one 16-byte load where they are there.
+// Past the list's end a lane gets -1.
+__device__ __forceinline__ Vec<int32_t, 4> load_ids(const int32_t *p, int64_t i, int64_t n) {
+  if (i + 4 <= n) return load_vec<int32_t, 4>(p + i);
+  Vec<int32_t, 4> x;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) f(x.v[e]);
-    } else {
-      for (int64_t q = i; q < n; ++q) f(p[q]);
-    }
-  }
+  for (int e = 0; e < 4; ++e) x.v[e] = i + e < n ? p[i + e] : -1;
+  return x;
 }
 
-// One workgroup per row and slab of S logits.  The slab's logits and mask bits
-// are loaded first; while they are on their way the row's whole history is
-// read and what falls into the slab is counted in LDS, one word per token:
-// its count among the generated IDs, a bit for the prompt, a bit for a bias.
-// Then each thread finishes its own logits.  A row's history is read once per
-// slab (from L2), so that no counts of rows * vocab words exist in memory.
+// One workgroup per row and slab of S logits, in three steps.
+// 1. The logits are loaded; while they are on their way the row's whole lists
+//    are read (each thread's first IDs of all three together) and what falls
+//    into the slab is counted in LDS, one word per token: its count among the
+//    generated IDs, a bit for the prompt, a bit and a slot for a bias.  Who
+//    counts a token first queues it.
+// 2. The queued tokens, side by side in full waves, get their logits, which go
+//    where their counts were, and a bit each that says so.
+// 3. Each thread takes its own logits, or those of step 2, masks and stores
+//    them.
+// A row's lists are read once per slab (from L2), so that no counts of rows *
+// vocab words exist in memory.  Left in step 3, the divisions and searches of
+// step 2 are executed for nearly every vector of a wave for one lane's sake.
 template <typename TI, typename TO, int S>
-__global__ void __launch_bounds__(LWG) k_logits(bpe_logits_args a) {
-  constexpr int E = 4;                 // logits per vector: 16 bytes of float32
-  constexpr int U = S / (LWG * E);     // vectors per thread
-  __shared__ uint32_t tab[S];
+__global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
+  constexpr int NT = kLogitThreads;
+  constexpr int E = 4;             // logits per vector: 16 bytes of float32
+  constexpr int U = S / (NT * E);  // vectors per thread
+  constexpr int LU = 4, STEP = NT * 4;  // list loads in flight, IDs per step
+  __shared__ __align__(16) uint32_t tab[S];
+  __shared__ __align__(16) uint32_t done[S / 32];
+  __shared__ uint16_t queue[S];
+  __shared__ float biases[kBiasSlots];
+  __shared__ int32_t queued;
   const int tid = threadIdx.x;
   // a row's slabs are `rows` workgroups apart: where that is a multiple of the
-  // XCDs' number they run on one XCD and share the row's history in its L2
-  const unsigned slab = blockIdx.x / (unsigned)a.rows;
-  const int64_t b = blockIdx.x - slab * (unsigned)a.rows;
-  const int64_t v0 = (int64_t)slab * S;
+  // XCDs' number they are on one XCD and share the row's lists in its L2
+  const uint32_t slab = blockIdx.x / (uint32_t)a.rows;
+  const int64_t b = blockIdx.x - slab * (uint32_t)a.rows;
+  const uint32_t v0 = slab * S;
   const int n = (int)min<int64_t>(S, a.vocab - v0);
   const TI *x = (const TI *)a.logits + b * a.logits_stride + v0;
   Vec<TI, E> in[U];
+  if (n == S) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = (u * LWG + tid) * E;
-    if (c + E <= n) {
-      in[u] = load_vec<TI, E>(x + c);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) in[u].v[e] = c + e < n ? x[c + e] : (TI)0.f;
-    }
+    for (int u = 0; u < U; ++u) in[u] = load_vec<TI, E>(x + (u * NT + tid) * E);
   }
   uint32_t status = 0;
-  uint32_t allow[U];
+  bool bad_off = false, bad_id = false;
+  int64_t plo = 0, phi = 0, blo = 0, bhi = 0, made = 0;
+  if (a.prompt_off) ragged(a.prompt_off, b, a.n_prompt, &plo, &phi, &bad_off);
+  if (a.bias_off) ragged(a.bias_off, b, a.n_bias, &blo, &bhi, &bad_off);
+  if (a.made_len) {
+    made = a.made_len[b];
+    if (made < 0 || made > a.made_width) {
+      status |= BPE_STATUS_BAD_LENGTH;
+      made = made < 0 ? 0 : a.made_width;
+    }
+  }
   int32_t mrow = a.mask_row ? a.mask_row[b] : -1;
-  if (a.mask_row && (mrow < -1 || mrow >= a.n_masks)) {
+  if (mrow < -1 || (a.mask_row && mrow >= a.n_masks)) {
     status |= BPE_STATUS_BAD_MASK_ROW;
     mrow = -1;
   }
+  const int32_t *pp = a.prompt_ids + plo, *mp = a.made_ids + b * a.made_stride;
+  const int64_t np = phi - plo, nb = bhi - blo;
+  const bool wide = nb > kBiasSlots;  // slots repeat: values are searched for
+  for (int i = tid * 4; i < S; i += NT * 4) lds_store16(&tab[i], u32x4{});
+  for (int i = tid * 4; i < S / 32; i += NT * 4) lds_store16(&done[i], u32x4{});
+  if (tid == 0) queued = 0;
+  Vec<int32_t, 4> p0[1], m0[1];
+  int32_t bv = -1, bprev = -1;
+  float bval = 0.f;
+  if (tid * 4 < np) p0[0] = load_ids(pp, tid * 4, np);
+  if (tid * 4 < made) m0[0] = load_ids(mp, tid * 4, made);
+  if (tid < nb) {
+    bv = a.bias_ids[blo + tid];
+    bval = a.bias_values[blo + tid];
+    if (tid > 0) bprev = a.bias_ids[blo + tid - 1];
+  }
+  uint32_t allow[U];
+  const uint32_t *mask = a.mask + mrow * a.mask_stride + (v0 >> 5);
+  if (mrow >= 0) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = (u * LWG + tid) * E;
-    allow[u] = ~0u;
-    if (mrow >= 0 && c < n)
-      allow[u] = a.mask[mrow * a.mask_stride + ((v0 + c) >> 5)] >> (c & 31);
+    for (int u = 0; u < U; ++u) {
+      const int c = (u * NT + tid) * E;
+      if (c < n) allow[u] = mask[c >> 5] >> (c & 31);
+    }
   }
-  const float rep = a.repetition ? a.repetition[b] : 1.f;
-  const float freq = a.frequency ? a.frequency[b] : 0.f;
-  const float pres = a.presence ? a.presence[b] : 0.f;
-  for (int i = tid * 4; i < S; i += LWG * 4) store_vec(&tab[i], Vec<uint32_t, 4>{});
   __syncthreads();
-  bool bad_off = false, bad_id = false;
-  if (a.prompt_off) {
-    int64_t lo, hi;
-    ragged(a.prompt_off, b, a.n_prompt, &lo, &hi, &bad_off);
-    each_id(a.prompt_ids + lo, hi - lo, [&](int32_t v) {
-      if (v >= v0 && v < v0 + n) tab[v - v0] = kPrompt;
-      bad_id |= v < 0 || v >= a.vocab;
-    });
-    __syncthreads();
-  }
-  if (a.made_len) {
-    int64_t len = a.made_len[b];
-    if (len < 0 || len > a.made_width) {
-      status |= BPE_STATUS_BAD_LENGTH;
-      len = len < 0 ? 0 : a.made_width;
+  auto enqueue = [&](uint32_t k, uint32_t before) {
+    if (before == 0) queue[atomicAdd(&queued, 1)] = (uint16_t)k;
+  };
+  // (the counts of all of a thread's IDs are in flight before the first answer
+  // is looked at)
+  auto count = [&](const auto &y, int64_t i, int64_t len, bool prompt) {
+    constexpr int L = sizeof(y) / sizeof(y[0]);
+    uint32_t before[L * 4];
+#pragma unroll
+    for (int l = 0; l < L * 4; ++l) {
+      const uint32_t k = (uint32_t)y[l / 4].v[l % 4] - v0;
+      before[l] = 1;
+      if (k < (uint32_t)n) before[l] = prompt ? atomicOr(&tab[k], kPrompt) : atomicAdd(&tab[k], 1u);
     }
-    each_id(a.made_ids + b * a.made_stride, len, [&](int32_t v) {
-      if (v >= v0 && v < v0 + n) atomicAdd(&tab[v - v0], 1u);
-      bad_id |= v < 0 || v >= a.vocab;
-    });
-  }
-  int64_t blo = 0, bhi = 0;
-  if (a.bias_off) {
-    ragged(a.bias_off, b, a.n_bias, &blo, &bhi, &bad_off);
-    for (int64_t i = blo + tid; i < bhi; i += LWG) {
-      const int32_t v = a.bias_ids[i];
-      if (v >= v0 && v < v0 + n) atomicOr(&tab[v - v0], kBiased);
-      bad_id |= v < 0 || v >= a.vocab;
-      if (i > blo && a.bias_ids[i - 1] >= v) status |= BPE_STATUS_BAD_BIAS;
+#pragma unroll
+    for (int l = 0; l < L * 4; ++l) enqueue((uint32_t)y[l / 4].v[l % 4] - v0, before[l]);
+    if (slab == 0) {
+#pragma unroll
+      for (int l = 0; l < L * 4; ++l)
+        bad_id |= (uint32_t)y[l / 4].v[l % 4] >= (uint32_t)a.vocab && i + l / 4 * STEP + l % 4 < len;
     }
+  };
+  auto bias = [&](int32_t v, int32_t prev, float val, int64_t i) {
+    const uint32_t k = (uint32_t)v - v0, slot = (uint32_t)i % kBiasSlots;
+    if (k < (uint32_t)n) {
+      enqueue(k, atomicOr(&tab[k], kBiased | slot << kSlotShift));
+      biases[slot] = val;
+    }
+    bad_id |= (uint32_t)v >= (uint32_t)a.vocab;
+    if (i > 0 && prev >= v) status |= BPE_STATUS_BAD_BIAS;
+  };
+  if (tid * 4 < np) count(p0, tid * 4, np, true);
+  if (tid * 4 < made) count(m0, tid * 4, made, false);
+  if (tid < nb) bias(bv, bprev, bval, tid);
+  for (int64_t i = STEP + tid * 4; i < np; i += STEP * LU) {
+    Vec<int32_t, 4> y[LU];
+#pragma unroll
+    for (int l = 0; l < LU; ++l) y[l] = load_ids(pp, i + l * STEP, np);
+    count(y, i, np, true);
   }
+  for (int64_t i = STEP + tid * 4; i < made; i += STEP) {
+    const Vec<int32_t, 4> y[1] = {load_ids(mp, i, made)};
+    count(y, i, made, false);
+  }
+  for (int64_t i = NT + tid; i < nb; i += NT)
+    bias(a.bias_ids[blo + i], a.bias_ids[blo + i - 1], a.bias_values[blo + i], i);
   if (slab == 0) {  // every slab sees the same lists: one reports
     if (bad_off) status |= BPE_STATUS_BAD_ID_OFFSETS;
     if (bad_id) status |= BPE_STATUS_BAD_ID;
     if (status) atomicOr(a.status, (int32_t)status);
   }
   __syncthreads();
-  TO *out = (TO *)a.out + b * a.out_stride + v0;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = (u * LWG + tid) * E;
-    if (c >= n) continue;
-    const Vec<uint32_t, E> t = load_vec<uint32_t, E>(&tab[c]);
-    Vec<TO, E> r;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      float y = (float)in[u].v[e];
-      const uint32_t w = t.v[e];
-      if (w) {
-        if (w & ~kBiased) y = y > 0.f ? y / rep : y * rep;
-        if (w & kCount) y -= freq * (float)(w & kCount) + pres;
-        if (w & kBiased) {
+  if (queued) {
+    const float rep = a.repetition ? a.repetition[b] : 1.f;
+    const float freq = a.frequency ? a.frequency[b] : 0.f;
+    const float pres = a.presence ? a.presence[b] : 0.f;
+    for (int j = tid; j < queued; j += NT) {
+      const uint32_t k = queue[j], w = tab[k];
+      float y = (float)x[k];
+      if (w & (kPrompt | kCount)) y = y > 0.f ? y / rep : y * rep;
+      if (w & kCount) y -= freq * (float)(w & kCount) + pres;
+      if (w & kBiased) {
+        // (two biases of one token, which the status reports, can mix slots)
+        float bias = 0.f;
+        if (!wide) {
+          const uint32_t slot = (w >> kSlotShift) % kBiasSlots;
+          if (slot < nb) bias = biases[slot];
+        } else {
           int64_t lo = blo, hi = bhi;  // the last entry with an ID <= v
           while (hi - lo > 1) {
             const int64_t mid = (lo + hi) >> 1;
-            if (a.bias_ids[mid] <= v0 + c + e) lo = mid;
+            if (a.bias_ids[mid] <= (int32_t)(v0 + k)) lo = mid;
             else hi = mid;
           }
-          y += a.bias_values[lo];
+          bias = a.bias_values[lo];
         }
+        y += bias;
       }
-      if (!((allow[u] >> e) & 1u)) y = -INFINITY;
-      r.v[e] = from_f32<TO>(y);
+      tab[k] = __float_as_uint(y);
+      atomicOr(&done[k >> 5], 1u << (k & 31));
     }
-    if (c + E <= n) {
-      store_vec<TO, E>(out + c, r);
-    } else {
+  }
+  __syncthreads();
+  TO *out = (TO *)a.out + b * a.out_stride + v0;
+  if (n == S) {
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (c + e < n) out[c + e] = r.v[e];
+    for (int u = 0; u < U; ++u) {
+      const int c = (u * NT + tid) * E;
+      const uint32_t bits = done[c >> 5] >> (c & 31) & 15u;
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = (float)in[u].v[e];
+      if (bits) {
+        const u32x4 t = lds_load16(&tab[c]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = (bits >> e) & 1u ? __uint_as_float(t[e]) : y[e];
+      }
+      if (mrow >= 0) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = (allow[u] >> e) & 1u ? y[e] : -INFINITY;
+      }
+      Vec<TO, E> r;
+#pragma unroll
+      for (int e = 0; e < E; ++e) r.v[e] = from_f32<TO>(y[e]);
+      store_vec<TO, E, XNTS>(out + c, r);
+    }
+  } else {
+    // the row's last slab, element by element
+    for (int c = tid; c < n; c += NT) {
+      float y = (float)x[c];
+      if ((done[c >> 5] >> (c & 31)) & 1u) y = __uint_as_float(tab[c]);
+      if (mrow >= 0 && !((mask[c >> 5] >> (c & 31)) & 1u)) y = -INFINITY;
+      out[c] = from_f32<TO>(y);
     }
   }
 }
@@ -163,8 +233,8 @@ __global__ void __launch_bounds__(LWG) k_logits(bpe_logits_args a) {
 template <typename TI, typename TO>
 hipError_t logits_as(const bpe_logits_args &a, hipStream_t stream) {
   constexpr int S = kLogitSlab;
-  hipLaunchKernelGGL((k_logits<TI, TO, S>),
-                     dim3((unsigned)((a.vocab + S - 1) / S * a.rows)), dim3(LWG), 0, stream, a);
+  hipLaunchKernelGGL((k_logits<TI, TO, S>), dim3((unsigned)((a.vocab + S - 1) / S * a.rows)),
+                     dim3(kLogitThreads), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -370,7 +370,7 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
     if used is None:
         used = torch.empty(1, dtype=torch.int64, device=dev)
     if workspace is None:
-        w_bytes = L.bpe_block_tables_workspace_bytes(R)
+        w_bytes = L.bpe_block_tables_workspace_bytes(R, n_new)
         workspace = torch.empty(w_bytes, dtype=torch.uint8, device=dev) if w_bytes else None
     else:
         w_bytes = workspace.numel() * workspace.element_size()

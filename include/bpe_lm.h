@@ -52,7 +52,7 @@ extern "C" {
 
 /* limits */
 #define BPE_MAX_WIDTH (1 << 18)             /* columns of an embedding table */
-#define BPE_MAX_ROWS ((int64_t)1 << 27)     /* rows of an embedding table, columns of logits */
+#define BPE_MAX_ROWS ((int64_t)1 << 26)     /* rows of an embedding table, columns of logits */
 #define BPE_MAX_IDS ((int64_t)1 << 30)      /* IDs per embedding call */
 
 /*
@@ -109,10 +109,10 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
  *  made_ids, made_len       int32 [rows][made_width] (made_stride apart) and
  *              int32 [rows]: the first made_len[b] IDs of row b count; a
  *              length outside [0, made_width] sets BPE_STATUS_BAD_LENGTH and
- *              is taken to the nearer end.
+ *              is taken to the nearer end.  made_width < 2^21.
  *  bias_ids, bias_values, bias_off   int32 / float [n_bias], int64 [rows + 1]:
  *              ragged; a row's IDs strictly increase, else BPE_STATUS_BAD_BIAS
- *              (and which bias a token gets is open).
+ *              (and what bias its tokens get is open).
  *  mask, mask_row   uint32 [n_masks][(vocab + 31) / 32] (mask_stride apart)
  *              and int32 [rows]: bit v & 31 of word v >> 5 of row mask_row[b]
  *              lets v through; -1: no mask.  Another row number outside
@@ -147,8 +147,8 @@ typedef struct {
 int bpe_process_logits(const bpe_logits_args *args, void *hip_stream);
 
 /* Workspace bytes bpe_block_tables needs (0 for few requests: d_workspace may
- * then be NULL). */
-size_t bpe_block_tables_workspace_bytes(int64_t n_requests);
+ * then be NULL; 8-byte aligned otherwise). */
+size_t bpe_block_tables_workspace_bytes(int64_t n_requests, int64_t n_new);
 
 /*
  * Places the new tokens of a batch of requests in a paged cache of blocks of

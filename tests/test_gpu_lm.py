@@ -95,6 +95,18 @@ def test_embed_strides_pad_bad_ids(D, wide):
         lm.embed(w, dev(ids), 1.0)
 
 
+@pytest.mark.parametrize("wt,ot", [(BF16, BF16), (F32, BF16), (F16, F32)])
+@pytest.mark.parametrize("n,D", [(33000, 512), (33001, 513), (17001, 1001), (4500, 4104)])
+def test_embed_large(n, D, wt, ot):
+    V = 300
+    w = randn((V, D), wt, 1)
+    ids = ids_of(n, V, n)
+    ids[::7] = 5
+    got = lm.embed(w, dev(ids), 0.3, pad_id=5, out_dtype=ot)
+    want = ref.embed(ref.f64(w), ids, float(np.float32(0.3)), 5)
+    ref.check(got, want, ref.U * np.abs(want), "embed")
+
+
 def test_embed_pad_outside_the_table():
     w = randn((10, 16), F32, 4)
     ids = np.array([3, 999, 9], np.int32)
@@ -145,7 +157,7 @@ def test_embed_grad(n, V, D, gt, ot):
 
 
 @pytest.mark.parametrize("kind", ["one", "distinct", "zipf"])
-@pytest.mark.parametrize("n", [1, 64, 4096, 4097, 20000, 70001])
+@pytest.mark.parametrize("n", [1, 9, 64, 2047, 2048, 2049, 4096, 4097, 20000, 70001])
 def test_embed_grad_lengths(n, kind):
     V, D = 1500, 72
     g = randn((n, D), BF16, n)
@@ -156,10 +168,11 @@ def test_embed_grad_lengths(n, kind):
     assert torch.equal(got, lm.embed_grad(g, dev(ids), V))  # the same bits again
 
 
-@pytest.mark.parametrize("D", [5, 513])
+@pytest.mark.parametrize("n", [100, 3001])
+@pytest.mark.parametrize("D", [5, 513, 2056])
 @pytest.mark.parametrize("ot", [F32, BF16])
-def test_embed_grad_accumulates(D, ot):
-    n, V = 3001, 200
+def test_embed_grad_accumulates(D, ot, n):
+    V = 200
     g = strided(randn((n, D), BF16, 1), 3)
     ids = ids_of(n, V, 2)
     ids[ids == 7] = 8  # a row without tokens
@@ -173,12 +186,13 @@ def test_embed_grad_accumulates(D, ot):
     assert torch.all(gaps(out, 5) == 0)
 
 
-def test_embed_grad_pad_and_bad_ids():
-    n, V, D = 5000, 100, 16
+@pytest.mark.parametrize("n", [1999, 5000])
+def test_embed_grad_pad_and_bad_ids(n):
+    V, D = 100, 16
     g = randn((n, D), F32, 1)
     ids = ids_of(n, V, 2)
     ids[::3] = 99
-    ids[1], ids[2], ids[4999] = -1, V, -2**31
+    ids[1], ids[2], ids[n - 1] = -1, V, -2**31
     g[0] = float("nan")  # a pad position
     st = status()
     got = lm.embed_grad(g, dev(ids), V, pad_id=99, status=st)
@@ -314,6 +328,21 @@ def test_logits_in_place_and_strided(V):
 def test_logits_long_history():
     x, args, want, tol = logits_case(3, 20000, F32, 5, prompt=30000, made=5000, bias=300)
     ref.check(lm.process_logits(x, **args), want, tol)
+
+
+@pytest.mark.parametrize("bias", [512, 513, 900, 4000])
+def test_logits_many_biases(bias):
+    x, args, want, tol = logits_case(4, 9000, F32, bias, bias=bias)
+    ref.check(lm.process_logits(x, **args), want, tol)
+    # and every one of the row's first IDs biased
+    n = min(bias, 9000)
+    off = torch.arange(5, device=device()) * n
+    ids = torch.arange(n, dtype=torch.int32, device=device()).repeat(4)
+    val = randn((4 * n,), F32, bias)
+    got = lm.process_logits(x, bias_off=off, bias_ids=ids, bias_values=val)
+    want = x.clone()
+    want[:, :n] += val.view(4, n)
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("keep", [(), ("prompt_ids", "prompt_off", "repetition"),
@@ -608,4 +637,5 @@ def test_refusals_on_the_device():
     with pytest.raises(TypeError, match="status"):
         lm.embed(w, ids, status=torch.zeros(1, dtype=torch.int64, device=device()))
     with pytest.raises(BPEError):
-        lm.embed_grad(randn((3, 16), F32, 1), ids, 10, workspace=torch.zeros(8, device=device()))
+        lm.embed_grad(randn((3000, 16), F32, 1), torch.zeros(3000, dtype=torch.int32, device=device()),
+                      10, workspace=torch.zeros(8, device=device()))
