@@ -85,14 +85,14 @@ struct FillShared {
   int64_t red[BWG / 64];
   int32_t wmax[BWG / 64];
   int32_t r0;
-  int32_t n_slow;            // groups of four tokens that are not of one request
-  int16_t slow[kBlockChunk / 4];
+  int32_t n_slow;            // pairs of tokens that are not of one request
+  int16_t slow[kBlockChunk / 2];
 };
 
 // The chunk's tokens.  The requests that start in it mark their first token;
-// a running maximum gives every token its request.  Then four neighbouring
-// tokens per thread and step: one lookup of the request (in LDS) and one
-// division where they are one request's; the few groups that are not are listed
+// a running maximum gives every token its request.  Then two neighbouring
+// tokens per thread and step, so that a wave stores whole lines: one lookup of the request (in LDS) and one
+// division where they are one request's; the few pairs that are not are listed
 // and done one token per thread afterwards (done in place they cost every wave
 // the slow path).  The token at a block's first place in the cache also enters
 // the block into the table: a new block's first place always belongs to a new
@@ -101,7 +101,7 @@ struct FillShared {
 // blocks of all tokens.
 // FUSED (R <= kBlockFused): each workgroup sums the requests' needs itself, one
 // launch in all.
-template <bool FUSED>
+template <bool FUSED, bool STREAM>
 __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
   __shared__ FillShared s;
   __shared__ int64_t before[FUSED ? kBlockFused : kBlockGroups];
@@ -207,61 +207,58 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
     auto enter = [&](int k, int32_t blk, int32_t block) {
       if (blk < a.width) a.table[(r0 + k) * a.stride + blk] = block;
     };
-    // Four neighbouring tokens of one request, in at most two blocks.  All
-    // loads of all steps go first (a wait for a load waits for the stores
-    // before it as well), unconditional ones, so that they are in flight
-    // together.
-    constexpr int STEPS = kBlockChunk / (4 * BWG);
+    // Two neighbouring tokens of one request, in at most two blocks.  All loads
+    // of all steps go first (a wait for a load waits for the stores before it
+    // as well), unconditional ones, so that they are in flight together.
+    constexpr int STEPS = kBlockChunk / (2 * BWG);
     const int32_t *none = (const int32_t *)a.off;
     int32_t kk[STEPS], pos[STEPS], blk[STEPS], b0[STEPS], b1[STEPS];
-    bool made0[STEPS];  // the first block is a new one
+    bool fresh[STEPS];  // the first block is a new one
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
-      const int i = (u * BWG + tid) * 4;
-      const u32x4 k = lds_load16(&s.req[i]);
-      const int kn = min((int)k.x, kNear - 1);
+      const int i = (u * BWG + tid) * 2;
+      const int k = s.req[i], kn = min(k, kNear - 1);
       const int64_t at64 = s.pos0[kn] + i, free0 = s.free0[kn];
       const int32_t have = s.have[kn];
-      const bool quad = i + 4 <= cnt && k.x == k.w && k.x < kNear && a.bs >= 4 && at64 >= 0 &&
-                        at64 <= INT32_MAX - 3;
-      kk[u] = quad ? (int32_t)k.x : -1;
-      pos[u] = quad ? (int32_t)at64 : 0;
+      const bool pair = i + 2 <= cnt && k == s.req[i + 1] && k < kNear && a.bs >= 2 && at64 >= 0 &&
+                        at64 < INT32_MAX;
+      kk[u] = pair ? k : -1;
+      pos[u] = pair ? (int32_t)at64 : 0;
       blk[u] = block_of(a, pos[u]);
-      made0[u] = blk[u] >= have;
-      const int32_t *p0 = quad ? look(k.x, blk[u], free0, have) : nullptr;
-      const int32_t *p1 = quad ? look(k.x, blk[u] + 1, free0, have) : nullptr;
+      fresh[u] = blk[u] >= have;
+      const int32_t *p0 = pair ? look(k, blk[u], free0, have) : nullptr;
+      const int32_t *p1 = pair ? look(k, blk[u] + 1, free0, have) : nullptr;
       b0[u] = *(p0 ? p0 : none);
       b1[u] = *(p1 ? p1 : none);
       b0[u] = p0 ? b0[u] : -1;
       b1[u] = p1 ? b1[u] : -1;
-      if (!quad && i < cnt) s.slow[atomicAdd(&s.n_slow, 1)] = (int16_t)i;
+      if (!pair && i < cnt) s.slow[atomicAdd(&s.n_slow, 1)] = (int16_t)i;
     }
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
       if (kk[u] < 0) continue;
-      const int i = (u * BWG + tid) * 4;
+      const int i = (u * BWG + tid) * 2;
       const int32_t at = pos[u] - blk[u] * a.bs;
-      if (at == 0 && made0[u]) enter(kk[u], blk[u], b0[u]);
+      const bool two = at + 1 == a.bs;
+      if (at == 0 && fresh[u]) enter(kk[u], blk[u], b0[u]);
       // (the second block's first place is a new token's: it is a new block)
-      if (at + 3 >= a.bs) enter(kk[u], blk[u] + 1, b1[u]);
+      if (two) enter(kk[u], blk[u] + 1, b1[u]);
+      if (blk[u] + two >= a.width) status |= BPE_STATUS_TABLE_FULL;
       const bool ok0 = b0[u] >= 0 && blk[u] < a.width, ok1 = b1[u] >= 0 && blk[u] + 1 < a.width;
-      if (blk[u] + (at + 3 >= a.bs) >= a.width) status |= BPE_STATUS_TABLE_FULL;
-      const int64_t s0 = (int64_t)b0[u] * a.bs + at, s1 = (int64_t)b1[u] * a.bs + (at - a.bs);
-      Vec<int64_t, 4> slot;
-      Vec<int32_t, 4> posn;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bool in0 = at + q < a.bs;
-        posn.v[q] = pos[u] + q;
-        slot.v[q] = (in0 ? ok0 : ok1) ? (in0 ? s0 : s1) + q : -1;
-      }
-      store_vec(a.slots + i0 + i, slot);
-      store_vec(a.positions + i0 + i, posn);
+      const int64_t s0 = (int64_t)b0[u] * a.bs + at, s1 = (int64_t)b1[u] * a.bs;
+      Vec<int64_t, 2> slot;
+      Vec<int32_t, 2> posn;
+      slot.v[0] = ok0 ? s0 : -1;
+      slot.v[1] = two ? (ok1 ? s1 : -1) : ok0 ? s0 + 1 : -1;
+      posn.v[0] = pos[u];
+      posn.v[1] = pos[u] + 1;
+      store_vec<int64_t, 2, STREAM>(a.slots + i0 + i, slot);
+      store_vec<int32_t, 2, STREAM>(a.positions + i0 + i, posn);
     }
     __syncthreads();
     // the others one by one, side by side
-    for (int j = tid; j < s.n_slow * 4; j += BWG) {
-      const int i = s.slow[j >> 2] + (j & 3);
+    for (int j = tid; j < s.n_slow * 2; j += BWG) {
+      const int i = s.slow[j >> 1] + (j & 1);
       if (i >= cnt) continue;
       const int k = s.req[i];
       int64_t at64, free0;
@@ -303,12 +300,15 @@ hipError_t launch_blocks(const BlockArgs &a, hipStream_t stream) {
     return hipGetLastError();
   }
   const unsigned chunks = a.T > 0 ? (unsigned)((a.T + kBlockChunk - 1) / kBlockChunk) : 1;
+  const bool big = a.T * 12 >= kStreamBytes;
   if (a.R <= kBlockFused) {
-    hipLaunchKernelGGL(k_block_fill<true>, dim3(chunks), dim3(BWG), 0, stream, a);
+    if (big) hipLaunchKernelGGL((k_block_fill<true, true>), dim3(chunks), dim3(BWG), 0, stream, a);
+    else hipLaunchKernelGGL((k_block_fill<true, false>), dim3(chunks), dim3(BWG), 0, stream, a);
   } else {
     const unsigned groups = (unsigned)(((a.R - 1) >> a.group_log2) + 1);
     hipLaunchKernelGGL(k_block_scan, dim3(groups), dim3(kBlockScan), 0, stream, a);
-    hipLaunchKernelGGL(k_block_fill<false>, dim3(chunks), dim3(BWG), 0, stream, a);
+    if (big) hipLaunchKernelGGL((k_block_fill<false, true>), dim3(chunks), dim3(BWG), 0, stream, a);
+    else hipLaunchKernelGGL((k_block_fill<false, false>), dim3(chunks), dim3(BWG), 0, stream, a);
   }
   return hipGetLastError();
 }

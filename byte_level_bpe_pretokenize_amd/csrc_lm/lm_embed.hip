@@ -517,7 +517,7 @@ hipError_t embed_as(EmbedArgs a, hipStream_t stream) {
 template <typename TI, typename TO>
 hipError_t embed_of(const EmbedArgs &a, hipStream_t stream) {
   if (a.width < 8) return embed_as<TI, TO, 1, false>(a, stream);
-  const bool big = a.n_ids * a.width * (int64_t)sizeof(TO) >= (32 << 20);
+  const bool big = a.n_ids * a.width * (int64_t)sizeof(TO) >= kStreamBytes;
   constexpr int E = 16 / sizeof(TO);
   return big ? embed_as<TI, TO, E, true>(a, stream) : embed_as<TI, TO, E, false>(a, stream);
 }

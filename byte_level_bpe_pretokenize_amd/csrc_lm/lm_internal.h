@@ -13,6 +13,10 @@ namespace bpe {
 // up to 512 a workgroup).
 constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
 
+// Outputs of at least this size are stored past the caches (they are larger
+// than the L2s together, so nothing of them is there when they are read).
+constexpr int64_t kStreamBytes = (int64_t)32 << 20;
+
 // ---- embedding ---------------------------------------------------------------
 struct EmbedArgs {
   const void *weight;
@@ -39,8 +43,8 @@ constexpr int kGradTile = 256;     // IDs per tile of the sums, at most
 constexpr int kGradDirect = 2048;  // IDs up to which no sort is made
 constexpr int kDigitBits = 9;
 constexpr int kMaxDigits = 1 << kDigitBits;
-constexpr int kSortThreads = 1024;
-constexpr int kSortTile = 4096;
+constexpr int kSortThreads = 512;
+constexpr int kSortTile = 4 * kSortThreads;
 
 struct GradArgs {
   const void *grad;
@@ -74,12 +78,7 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width);
 hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);
 
 // ---- logits ------------------------------------------------------------------
-#ifndef XSLAB
-#define XSLAB 4096
-#define XTH 256
-#endif
-constexpr int kLogitSlab = XSLAB;     // logits per workgroup
-constexpr int kLogitThreads = XTH;
+constexpr int kLogitPer = 16;  // logits per thread
 
 hipError_t launch_logits(const bpe_logits_args &a, hipStream_t stream);
 

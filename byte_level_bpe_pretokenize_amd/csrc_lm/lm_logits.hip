@@ -46,15 +46,16 @@ __device__ __forceinline__ Vec<int32_t, 4> load_ids(const int32_t *p, int64_t i,
 // A row's lists are read once per slab (from L2), so that no counts of rows *
 // vocab words exist in memory.  Left in step 3, the divisions and searches of
 // step 2 are executed for nearly every vector of a wave for one lane's sake.
-template <typename TI, typename TO, int S>
-__global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
-  constexpr int NT = kLogitThreads;
+template <typename TI, typename TO, int NT, bool STREAM>
+__global__ void __launch_bounds__(NT) k_logits(bpe_logits_args a) {
+  constexpr int S = NT * kLogitPer;
   constexpr int E = 4;             // logits per vector: 16 bytes of float32
   constexpr int U = S / (NT * E);  // vectors per thread
   constexpr int LU = 4, STEP = NT * 4;  // list loads in flight, IDs per step
   __shared__ __align__(16) uint32_t tab[S];
   __shared__ __align__(16) uint32_t done[S / 32];
-  __shared__ uint16_t queue[S];
+  constexpr int Q = S / 4;         // places in the queue
+  __shared__ uint16_t queue[Q];
   __shared__ float biases[kBiasSlots];
   __shared__ int32_t queued;
   const int tid = threadIdx.x;
@@ -89,6 +90,8 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
   }
   const int32_t *pp = a.prompt_ids + plo, *mp = a.made_ids + b * a.made_stride;
   const int64_t np = phi - plo, nb = bhi - blo;
+  // lists that do not fit one step: the words are looked at instead of a queue
+  const bool scan = np > STEP || made > STEP || nb > NT;
   const bool wide = nb > kBiasSlots;  // slots repeat: values are searched for
   for (int i = tid * 4; i < S; i += NT * 4) lds_store16(&tab[i], u32x4{});
   for (int i = tid * 4; i < S / 32; i += NT * 4) lds_store16(&done[i], u32x4{});
@@ -114,7 +117,9 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
   }
   __syncthreads();
   auto enqueue = [&](uint32_t k, uint32_t before) {
-    if (before == 0) queue[atomicAdd(&queued, 1)] = (uint16_t)k;
+    if (before != 0) return;
+    const int32_t at = atomicAdd(&queued, 1);
+    if (at < Q) queue[at] = (uint16_t)k;
   };
   // (the counts of all of a thread's IDs are in flight before the first answer
   // is looked at)
@@ -127,18 +132,34 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
       before[l] = 1;
       if (k < (uint32_t)n) before[l] = prompt ? atomicOr(&tab[k], kPrompt) : atomicAdd(&tab[k], 1u);
     }
+    if (!scan) {
 #pragma unroll
-    for (int l = 0; l < L * 4; ++l) enqueue((uint32_t)y[l / 4].v[l % 4] - v0, before[l]);
+      for (int l = 0; l < L * 4; ++l) enqueue((uint32_t)y[l / 4].v[l % 4] - v0, before[l]);
+    }
     if (slab == 0) {
 #pragma unroll
       for (int l = 0; l < L * 4; ++l)
         bad_id |= (uint32_t)y[l / 4].v[l % 4] >= (uint32_t)a.vocab && i + l / 4 * STEP + l % 4 < len;
     }
   };
+  // the same for a list too long for the queue: no answers
+  auto count_only = [&](const auto &y, int64_t i, int64_t len, bool prompt) {
+    constexpr int L = sizeof(y) / sizeof(y[0]);
+#pragma unroll
+    for (int l = 0; l < L * 4; ++l) {
+      const uint32_t id = (uint32_t)y[l / 4].v[l % 4], k = id - v0;
+      if (k < (uint32_t)n) {
+        if (prompt) atomicOr(&tab[k], kPrompt);
+        else atomicAdd(&tab[k], 1u);
+      }
+      if (slab == 0) bad_id |= id >= (uint32_t)a.vocab && i + l / 4 * STEP + l % 4 < len;
+    }
+  };
   auto bias = [&](int32_t v, int32_t prev, float val, int64_t i) {
     const uint32_t k = (uint32_t)v - v0, slot = (uint32_t)i % kBiasSlots;
     if (k < (uint32_t)n) {
-      enqueue(k, atomicOr(&tab[k], kBiased | slot << kSlotShift));
+      const uint32_t before = atomicOr(&tab[k], kBiased | slot << kSlotShift);
+      if (!scan) enqueue(k, before);
       biases[slot] = val;
     }
     bad_id |= (uint32_t)v >= (uint32_t)a.vocab;
@@ -151,11 +172,11 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
     Vec<int32_t, 4> y[LU];
 #pragma unroll
     for (int l = 0; l < LU; ++l) y[l] = load_ids(pp, i + l * STEP, np);
-    count(y, i, np, true);
+    count_only(y, i, np, true);
   }
   for (int64_t i = STEP + tid * 4; i < made; i += STEP) {
     const Vec<int32_t, 4> y[1] = {load_ids(mp, i, made)};
-    count(y, i, made, false);
+    count_only(y, i, made, false);
   }
   for (int64_t i = NT + tid; i < nb; i += NT)
     bias(a.bias_ids[blo + i], a.bias_ids[blo + i - 1], a.bias_values[blo + i], i);
@@ -165,13 +186,12 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
     if (status) atomicOr(a.status, (int32_t)status);
   }
   __syncthreads();
-  if (queued) {
+  if (scan || queued) {
     const float rep = a.repetition ? a.repetition[b] : 1.f;
     const float freq = a.frequency ? a.frequency[b] : 0.f;
     const float pres = a.presence ? a.presence[b] : 0.f;
-    for (int j = tid; j < queued; j += NT) {
-      const uint32_t k = queue[j], w = tab[k];
-      float y = (float)x[k];
+    // the logit of the slab's token k, whose word is w
+    auto listed = [&](float y, uint32_t w, uint32_t k) {
       if (w & (kPrompt | kCount)) y = y > 0.f ? y / rep : y * rep;
       if (w & kCount) y -= freq * (float)(w & kCount) + pres;
       if (w & kBiased) {
@@ -191,8 +211,30 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
         }
         y += bias;
       }
-      tab[k] = __float_as_uint(y);
-      atomicOr(&done[k >> 5], 1u << (k & 31));
+      return y;
+    };
+    if (scan || queued > Q) {
+#pragma unroll 1
+      for (int u = 0; u < U; ++u) {
+        const int c = (u * NT + tid) * E;
+        if (c >= n) break;
+        const u32x4 t = lds_load16(&tab[c]);
+        uint32_t bits = 0;
+#pragma unroll 1
+        for (int e = 0; e < E; ++e) {
+          const uint32_t w = e == 0 ? t.x : e == 1 ? t.y : e == 2 ? t.z : t.w;
+          if (w == 0) continue;
+          tab[c + e] = __float_as_uint(listed((float)x[c + e], w, c + e));
+          bits |= 1u << e;
+        }
+        if (bits) atomicOr(&done[c >> 5], bits << (c & 31));
+      }
+    } else {
+      for (int j = tid; j < queued; j += NT) {
+        const uint32_t k = queue[j];
+        tab[k] = __float_as_uint(listed((float)x[k], tab[k], k));
+        atomicOr(&done[k >> 5], 1u << (k & 31));
+      }
     }
   }
   __syncthreads();
@@ -217,7 +259,7 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
       Vec<TO, E> r;
 #pragma unroll
       for (int e = 0; e < E; ++e) r.v[e] = from_f32<TO>(y[e]);
-      store_vec<TO, E, XNTS>(out + c, r);
+      store_vec<TO, E, STREAM>(out + c, r);
     }
   } else {
     // the row's last slab, element by element
@@ -230,12 +272,29 @@ __global__ void __launch_bounds__(kLogitThreads) k_logits(bpe_logits_args a) {
   }
 }
 
+template <typename TI, typename TO, int NT, bool STREAM>
+hipError_t logits_launch(const bpe_logits_args &a, hipStream_t stream) {
+  constexpr int S = NT * kLogitPer;
+  hipLaunchKernelGGL((k_logits<TI, TO, NT, STREAM>),
+                     dim3((unsigned)((a.vocab + S - 1) / S * a.rows)), dim3(NT), 0, stream, a);
+  return hipGetLastError();
+}
+
+// Long lists are read by wide workgroups, in half as many slabs (24 rows of
+// 100,256 logits with 26,000 prompt IDs each: 20 us with 512 threads, 26 with
+// 256); short ones leave narrow workgroups ahead (256 rows of 128,256 with 600:
+// 46 and 42 us).
+template <typename TI, typename TO, bool STREAM>
+hipError_t logits_wide(const bpe_logits_args &a, hipStream_t stream) {
+  const bool longer = a.n_prompt / a.rows + a.made_width > 4096;
+  return longer ? logits_launch<TI, TO, 512, STREAM>(a, stream)
+                : logits_launch<TI, TO, 256, STREAM>(a, stream);
+}
+
 template <typename TI, typename TO>
 hipError_t logits_as(const bpe_logits_args &a, hipStream_t stream) {
-  constexpr int S = kLogitSlab;
-  hipLaunchKernelGGL((k_logits<TI, TO, S>), dim3((unsigned)((a.vocab + S - 1) / S * a.rows)),
-                     dim3(kLogitThreads), 0, stream, a);
-  return hipGetLastError();
+  const bool big = a.rows * a.vocab * (int64_t)sizeof(TO) >= kStreamBytes;
+  return big ? logits_wide<TI, TO, true>(a, stream) : logits_wide<TI, TO, false>(a, stream);
 }
 
 template <typename TI>

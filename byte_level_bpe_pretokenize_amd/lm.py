@@ -30,6 +30,9 @@ _stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurr
     else lambda dev: torch.cuda.current_stream(dev).cuda_stream
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _type(t: torch.dtype, what: str) -> int:
     try:
         return _TYPES[t]
@@ -37,17 +40,21 @@ def _type(t: torch.dtype, what: str) -> int:
         raise TypeError(f"{what}: float32, bfloat16 or float16 expected, got {t}") from None
 
 
-def _flat(t: torch.Tensor, dtype: torch.dtype, what: str) -> int:
-    """The pointer of a contiguous tensor (0 where it is empty)."""
-    if t.dtype != dtype:
-        raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor")
+def _list(t: torch.Tensor, dtype: torch.dtype, n: int, what: str) -> int:
+    """The pointer of a contiguous tensor of n entries (n < 0: of any number)."""
+    if t.dtype is not dtype or not t.is_contiguous() or (n >= 0 and t.numel() != n):
+        if t.dtype is not dtype:
+            raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous tensor")
+        raise ValueError(f"{what}: {n} entries expected, got {t.numel()}")
     return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, what: str) -> int:
     """The row stride of a matrix whose rows are consecutive elements."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t.shape[1]
     if t.dim() != 2:
         raise ValueError(f"{what}: expected a matrix, got {t.dim()} dimensions")
     n, m = t.shape
@@ -67,15 +74,18 @@ def _int32(x: int, lo: int, what: str) -> int:
     return int(x)
 
 
-def _device(name: str, *tensors) -> int:
+def _device(name: str, tensors) -> int:
     """The current device's index; refuses tensors that are elsewhere."""
-    if not torch.cuda.is_initialized() and not torch.cuda.is_available():
-        raise RuntimeError("libbpe needs a HIP device; none is visible")
-    dev = torch.cuda.current_device()
+    dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name}: expected tensors on the current device (cuda:{dev}), "
-                             f"got one on {t.device}")
+            raise ValueError(f"{name}: expected tensors on the current device, got one on {t.device}")
+    if dev < 0:
+        if not torch.cuda.is_available():
+            raise RuntimeError("libbpe needs a HIP device; none is visible")
+        raise ValueError(f"{name}: expected tensors on the current device, got one on the host")
+    if dev != _current_device():
+        raise ValueError(f"{name}: expected tensors on the current device, got one on cuda:{dev}")
     return dev
 
 
@@ -124,7 +134,7 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
     pad_id = _int32(pad_id, -1, "pad_id")
     wt = _type(weight.dtype, "weight")
     ws = _rows(weight, "weight")
-    ip = _flat(ids, torch.int32, "ids")
+    ip = _list(ids, torch.int32, -1, "ids")
     n, (V, D) = ids.numel(), weight.shape
     if out is None:
         dt = weight.dtype if out_dtype is None else out_dtype
@@ -133,7 +143,7 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
         ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
         if tuple(out.shape) != (n, D) or out_dtype not in (None, out.dtype):
             raise ValueError(f"out: ({n}, {D}) of out_dtype expected, got {tuple(out.shape)}")
-    dev = _device("embed", weight, ids, out, status)
+    dev = _device("embed", (weight, ids, out, status))
     st = _status(status, dev)
     res = torch.empty((*ids.shape, D), dtype=dt, device=dev) if out is None else out
     rc = _lib.load().bpe_embed(weight.data_ptr(), wt, V, D, ws, ip, n, scale, pad_id,
@@ -164,7 +174,7 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float 
                    workspace=workspace, status=status)
     pad_id = _int32(pad_id, -1, "pad_id")
     gt = _type(grad.dtype, "grad")
-    ip = _flat(ids, torch.int32, "ids")
+    ip = _list(ids, torch.int32, -1, "ids")
     n = ids.numel()
     if grad.dim() != 2:
         if grad.shape[:-1] != ids.shape:
@@ -186,7 +196,7 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float 
             raise ValueError(f"out: ({n_rows}, {D}) of out_dtype expected, got {tuple(out.shape)}")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
-    dev = _device("embed_grad", grad, ids, out, workspace, status)
+    dev = _device("embed_grad", (grad, ids, out, workspace, status))
     L = _lib.load()
     st = _status(status, dev)
     res = torch.empty((n_rows, D), dtype=dt, device=dev) if out is None else out
@@ -254,42 +264,46 @@ def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = No
     lt, ls = _type(logits.dtype, "logits"), _rows(logits, "logits")
     B, V = logits.shape
 
-    def of(t, dtype, n, what):
-        if t is None:
-            return None
-        p = _flat(t, dtype, what)
-        if t.numel() != n:
-            raise ValueError(f"{what}: {n} entries expected, got {t.numel()}")
-        return p
-
-    def together(what, *ts):
-        if any((t is None) != (ts[0] is None) for t in ts):
-            raise ValueError(f"{what} come together")
-
-    together("prompt_ids and prompt_off", prompt_ids, prompt_off)
-    together("out_ids and out_len", out_ids, out_len)
-    together("bias_off, bias_ids and bias_values", bias_off, bias_ids, bias_values)
-    together("mask and mask_row", mask, mask_row)
-    n_prompt = 0 if prompt_ids is None else prompt_ids.numel()
-    n_bias = 0 if bias_ids is None else bias_ids.numel()
-    pp = of(prompt_ids, torch.int32, n_prompt, "prompt_ids")
-    po = of(prompt_off, torch.int64, B + 1, "prompt_off")
-    m_ptr, m_width, m_stride = None, 0, 0
-    if out_ids is not None:
-        if out_ids.dtype != torch.int32:
+    pp = po = mp = ml = bo = bi = bv = kp = kr = None
+    n_prompt = m_width = m_stride = n_bias = k_rows = k_stride = 0
+    if prompt_off is not None and prompt_ids is not None:
+        n_prompt = prompt_ids.numel()
+        pp = _list(prompt_ids, torch.int32, n_prompt, "prompt_ids")
+        po = _list(prompt_off, torch.int64, B + 1, "prompt_off")
+    elif prompt_off is not None or prompt_ids is not None:
+        raise ValueError("prompt_ids and prompt_off come together")
+    if out_ids is not None and out_len is not None:
+        if out_ids.dtype is not torch.int32:
             raise TypeError(f"out_ids: torch.int32 expected, got {out_ids.dtype}")
         m_stride = _rows(out_ids, "out_ids")
-        if out_ids.shape[0] != B:
-            raise ValueError(f"out_ids: {B} rows expected, got {out_ids.shape[0]}")
-        m_ptr, m_width = out_ids.data_ptr(), out_ids.shape[1]
-    k_ptr, k_rows, k_stride = None, 0, 0
-    if mask is not None:
-        if mask.dtype not in (torch.int32, torch.uint32):
+        m_rows, m_width = out_ids.shape
+        if m_rows != B:
+            raise ValueError(f"out_ids: {B} rows expected, got {m_rows}")
+        mp = out_ids.data_ptr()
+        ml = _list(out_len, torch.int32, B, "out_len")
+    elif out_ids is not None or out_len is not None:
+        raise ValueError("out_ids and out_len come together")
+    if bias_off is not None and bias_ids is not None and bias_values is not None:
+        n_bias = bias_ids.numel()
+        bo = _list(bias_off, torch.int64, B + 1, "bias_off")
+        bi = _list(bias_ids, torch.int32, n_bias, "bias_ids")
+        bv = _list(bias_values, torch.float32, n_bias, "bias_values")
+    elif bias_off is not None or bias_ids is not None or bias_values is not None:
+        raise ValueError("bias_off, bias_ids and bias_values come together")
+    if mask is not None and mask_row is not None:
+        if mask.dtype is not torch.int32 and mask.dtype is not torch.uint32:
             raise TypeError(f"mask: torch.int32 expected, got {mask.dtype}")
         k_stride = _rows(mask, "mask")
-        if mask.shape[1] != (V + 31) // 32:
-            raise ValueError(f"mask: {(V + 31) // 32} words a row expected, got {mask.shape[1]}")
-        k_ptr, k_rows = mask.data_ptr(), mask.shape[0]
+        k_rows, words = mask.shape
+        if words != (V + 31) // 32:
+            raise ValueError(f"mask: {(V + 31) // 32} words a row expected, got {words}")
+        kp = mask.data_ptr()
+        kr = _list(mask_row, torch.int32, B, "mask_row")
+    elif mask is not None or mask_row is not None:
+        raise ValueError("mask and mask_row come together")
+    rp = None if repetition is None else _list(repetition, torch.float32, B, "repetition")
+    fp = None if frequency is None else _list(frequency, torch.float32, B, "frequency")
+    sp = None if presence is None else _list(presence, torch.float32, B, "presence")
     if out is None:
         dt = logits.dtype if out_dtype is None else out_dtype
         ot, os_ = _type(dt, "out_dtype"), V
@@ -297,20 +311,12 @@ def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = No
         ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
         if out.shape != logits.shape or out_dtype not in (None, out.dtype):
             raise ValueError(f"out: {tuple(logits.shape)} of out_dtype expected, got {tuple(out.shape)}")
-    args = (of(out_len, torch.int32, B, "out_len"),
-            of(repetition, torch.float32, B, "repetition"),
-            of(frequency, torch.float32, B, "frequency"),
-            of(presence, torch.float32, B, "presence"),
-            of(bias_ids, torch.int32, n_bias, "bias_ids"),
-            of(bias_values, torch.float32, n_bias, "bias_values"), n_bias,
-            of(bias_off, torch.int64, B + 1, "bias_off"),
-            k_ptr, k_rows, k_stride, of(mask_row, torch.int32, B, "mask_row"))
-    dev = _device("process_logits", logits, prompt_ids, prompt_off, out_ids, out_len, repetition,
-                  frequency, presence, bias_off, bias_ids, bias_values, mask, mask_row, out, status)
+    dev = _device("process_logits", (logits, prompt_ids, prompt_off, out_ids, out_len, repetition,
+                  frequency, presence, bias_off, bias_ids, bias_values, mask, mask_row, out, status))
     st = _status(status, dev)
     res = torch.empty((B, V), dtype=dt, device=dev) if out is None else out
-    a = _lib.LogitsArgs(logits.data_ptr(), ls, B, V, pp, n_prompt, po, m_ptr, m_width, m_stride,
-                        *args, res.data_ptr(), os_, st.data_ptr(), lt, ot)
+    a = _lib.LogitsArgs(logits.data_ptr(), ls, B, V, pp, n_prompt, po, mp, m_width, m_stride, ml,
+                        rp, fp, sp, bi, bv, n_bias, bo, kp, k_rows, k_stride, kr, res.data_ptr(), os_, st.data_ptr(), lt, ot)
     rc = _lib.load().bpe_process_logits(C.byref(a), _stream(dev))
     _end("bpe_process_logits", rc, st if status is None else None)
     return res
@@ -334,31 +340,31 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
                   workspace=workspace, status=status)
         return _on(stream, block_tables, (new_off, cached, free_blocks, table, *kw.values()),
                    new_off, n_new, cached, free_blocks, table, block_size, **kw)
-    op = _flat(new_off, torch.int64, "new_off")
-    cp = _flat(cached, torch.int32, "cached")
-    fp = _flat(free_blocks, torch.int32, "free_blocks")
     R = cached.numel()
-    if new_off.numel() != R + 1:
-        raise ValueError(f"new_off: {R + 1} entries expected, got {new_off.numel()}")
-    if table.dtype != torch.int32:
+    op = _list(new_off, torch.int64, R + 1, "new_off")
+    cp = _list(cached, torch.int32, R, "cached")
+    fp = _list(free_blocks, torch.int32, -1, "free_blocks")
+    if table.dtype is not torch.int32:
         raise TypeError(f"table: torch.int32 expected, got {table.dtype}")
     ts = _rows(table, "table")
-    if table.shape[0] != R:
-        raise ValueError(f"table: {R} rows expected, got {table.shape[0]}")
-    for t, dtype, n, what in ((slots, torch.int64, n_new, "slots"),
-                              (positions, torch.int32, n_new, "positions"),
-                              (lengths, torch.int32, R, "lengths"), (used, torch.int64, 1, "used")):
-        if t is not None:
-            _flat(t, dtype, what)
-            if t.numel() != n:
-                raise ValueError(f"{what}: {n} entries expected, got {t.numel()}")
+    t_rows, t_width = table.shape
+    if t_rows != R:
+        raise ValueError(f"table: {R} rows expected, got {t_rows}")
+    if slots is not None:
+        _list(slots, torch.int64, n_new, "slots")
+    if positions is not None:
+        _list(positions, torch.int32, n_new, "positions")
+    if lengths is not None:
+        _list(lengths, torch.int32, R, "lengths")
+    if used is not None:
+        _list(used, torch.int64, 1, "used")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor")
     block_size = _int32(block_size, 1, "block_size")
     if n_new < 0:
         raise ValueError(f"n_new: {n_new} is out of range")
-    dev = _device("block_tables", new_off, cached, free_blocks, table, slots, positions, lengths,
-                  used, workspace, status)
+    dev = _device("block_tables", (new_off, cached, free_blocks, table, slots, positions, lengths,
+                  used, workspace, status))
     L = _lib.load()
     st = _status(status, dev)
     if slots is None:
@@ -375,7 +381,7 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
     else:
         w_bytes = workspace.numel() * workspace.element_size()
     rc = L.bpe_block_tables(op, R, n_new, cp, fp, free_blocks.numel(), table.data_ptr(),
-                            table.shape[1], ts, block_size, slots.data_ptr(), positions.data_ptr(),
+                            t_width, ts, block_size, slots.data_ptr(), positions.data_ptr(),
                             lengths.data_ptr(), used.data_ptr(),
                             None if workspace is None else workspace.data_ptr(), w_bytes,
                             st.data_ptr(), _stream(dev))
