@@ -214,7 +214,7 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
   int s = 0;
   while (((int64_t)1 << s) < block_size) ++s;
   a.magic = (uint32_t)(((uint64_t)1 << (31 + s)) / (uint64_t)block_size + 1);
-  a.shift = 31 + s;
+  a.shift = s - 1;  // of the product's upper half
   a.slots = d_slots;
   a.positions = d_positions;
   a.lengths = d_lengths;

@@ -9,7 +9,7 @@ constexpr int BWG = 256;
 
 // x / block size, 0 <= x < 2^31.
 __device__ __forceinline__ int32_t block_of(const BlockArgs &a, int32_t x) {
-  return (int32_t)(((uint64_t)(uint32_t)x * a.magic) >> a.shift);
+  return a.bs == 1 ? x : (int32_t)(__umulhi((uint32_t)x, a.magic) >> a.shift);
 }
 
 // Blocks of the first len tokens.
@@ -76,33 +76,43 @@ __global__ void __launch_bounds__(kBlockScan) k_block_scan(BlockArgs a) {
 }
 
 constexpr int kNear = 256;  // requests of a chunk whose data is kept in LDS
+constexpr int32_t kFar = INT32_MAX;
+
+// Request r0 + k as the pairs of tokens want it: a token's position less its
+// place in the chunk, the blocks that were there (kFar: some position is not in
+// [0, INT32_MAX)), and the place of its block b in the list of free ones, less b.
+struct alignas(16) Near {
+  int32_t pos0, have;
+  int64_t free0;
+};
 
 struct FillShared {
   alignas(16) int32_t req[kBlockChunk];  // the request that starts at a token, then each token's, less r0
-  int64_t pos0[kNear];       // of request r0 + k: position of a token less its place in the chunk
-  int64_t free0[kNear];      // place of its block b in the list of free blocks, less b
-  int32_t have[kNear];       // blocks that were there
+  Near near[kNear];
   int64_t red[BWG / 64];
   int32_t wmax[BWG / 64];
   int32_t r0;
-  int32_t n_slow;            // pairs of tokens that are not of one request
+  int32_t n_slow;            // pairs of tokens left for the end
   int16_t slow[kBlockChunk / 2];
 };
 
 // The chunk's tokens.  The requests that start in it mark their first token;
 // a running maximum gives every token its request.  Then two neighbouring
-// tokens per thread and step, so that a wave stores whole lines: one lookup of the request (in LDS) and one
-// division where they are one request's; the few pairs that are not are listed
-// and done one token per thread afterwards (done in place they cost every wave
-// the slow path).  The token at a block's first place in the cache also enters
-// the block into the table: a new block's first place always belongs to a new
-// token.  What bounds it is arithmetic and the chain of dependent loads in each
-// workgroup, kept to four: the chunk's request, the requests, their groups, the
-// blocks of all tokens.
+// tokens per thread and step, so that a wave stores whole lines: where they are
+// one request's and in new blocks, one read of the request (from LDS), one
+// multiply-high for the block and one load of its number and the next one's.
+// The few pairs that are not (two requests', a block that was partly filled,
+// the ends of the table and of the free blocks) are listed and done one token
+// per thread afterwards; done in place they cost every wave that path.  The
+// token at a block's first place in the cache also enters the block into the
+// table: a new block's first place always belongs to a new token.  What bounds
+// it is the chain of dependent loads in each workgroup, kept to four (the
+// chunk's request, the requests, their groups, the blocks of all tokens), and
+// the arithmetic: XX us for 12.5 M tokens of 65,536 requests, 157 MB.
 // FUSED (R <= kBlockFused): each workgroup sums the requests' needs itself, one
 // launch in all.
 template <bool FUSED, bool STREAM>
-__global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
+__global__ void __launch_bounds__(BWG, FUSED ? 4 : 8) k_block_fill(BlockArgs a) {
   __shared__ FillShared s;
   __shared__ int64_t before[FUSED ? kBlockFused : kBlockGroups];
   const int tid = threadIdx.x;
@@ -148,11 +158,25 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
     __syncthreads();
     r0 = s.r0;
   } else {
-    static_assert(kBlockGroups == BWG, "one group per thread");
     // (the chunk's request is not set where the offsets are not valid)
     if (cnt > 0) r0 = min(max<int64_t>(a.chunk_req[blockIdx.x], 0), a.R - 1);
-    const int64_t groups = ((a.R - 1) >> a.group_log2) + 1;
-    before[tid] = block_excl_sum<int64_t, BWG>(tid < groups ? a.gsum[tid] : 0, s.red, &used);
+    if (uniform_wave_id() == 0) {  // the groups' running sums
+      static_assert(kBlockGroups == 256, "four groups per lane");
+      const int groups = (int)((a.R - 1) >> a.group_log2) + 1;
+      int64_t g[4], sum = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = tid * 4 + j < groups ? a.gsum[tid * 4 + j] : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += g[j];
+      used = wave_incl_sum(sum);
+      int64_t ex = used - sum;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        before[tid * 4 + j] = ex;
+        ex += g[j];
+      }
+      used = lane_value(used, 63);
+    }
     __syncthreads();
   }
   if (blockIdx.x == 0 && tid == 0) {
@@ -160,6 +184,8 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
     if (used > a.n_free) status |= BPE_STATUS_NO_BLOCKS;
   }
   if (cnt > 0) {
+    // request r's first token's position less its place in the chunk, and the
+    // place of its block b in the list of free ones, less b
     auto place = [&](int64_t r, int64_t lo, int32_t cached, int64_t first, int64_t *pos0,
                      int64_t *free0, int32_t *have) {
       cached = max(cached, 0);
@@ -174,11 +200,15 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
       const int32_t cached = a.cached[r];
       const int64_t first = FUSED ? 0 : a.first[r];
       const int64_t p = r0 + k < a.R ? lo - i0 : cnt;
-      if (p < cnt || k == 0) {
-        if (k < kNear) place(r, lo, cached, first, &s.pos0[k], &s.free0[k], &s.have[k]);
-        if (p > 0 && p < cnt) atomicMax(&s.req[p], (int32_t)k);
+      if (k < kNear) {
+        int64_t pos0, free0;
+        int32_t have;
+        place(r, lo, cached, first, &pos0, &free0, &have);
+        const bool in = pos0 + max<int64_t>(p, 0) >= 0 && pos0 + kBlockChunk < INT32_MAX;
+        s.near[k] = Near{(int32_t)pos0, in ? have : kFar, free0};
       }
-      if (!__syncthreads_or(p < cnt)) break;
+      if (p > 0 && p < cnt) atomicMax(&s.req[p], (int32_t)k);
+      if (!__syncthreads_or(tid == BWG - 1 && p < cnt)) break;  // (they increase)
     }
     constexpr int PER = kBlockChunk / BWG;
     int32_t v[PER];
@@ -196,42 +226,25 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) s.req[tid * PER + j] = max(v[j], left);
     __syncthreads();
-    // Block blk of request r0 + k: where its number stands (the table, for a
-    // block that was there, or the list of free ones), or nullptr for none.
-    auto look = [&](int k, int32_t blk, int64_t free0, int32_t have) -> const int32_t * {
-      const int64_t f = free0 + blk;
-      if (blk < have) return blk < a.width ? a.table + (r0 + k) * a.stride + blk : nullptr;
-      return f < a.n_free ? a.free_blocks + f : nullptr;
-    };
-    // Its first token enters it.
-    auto enter = [&](int k, int32_t blk, int32_t block) {
-      if (blk < a.width) a.table[(r0 + k) * a.stride + blk] = block;
-    };
-    // Two neighbouring tokens of one request, in at most two blocks.  All loads
-    // of all steps go first (a wait for a load waits for the stores before it
-    // as well), unconditional ones, so that they are in flight together.
+    // Two neighbouring tokens of one request, in one or two new blocks.  All
+    // loads of all steps go first (a wait for a load waits for the stores
+    // before it as well), unconditional ones, so that they are in flight
+    // together.
     constexpr int STEPS = kBlockChunk / (2 * BWG);
-    const int32_t *none = (const int32_t *)a.off;
-    int32_t kk[STEPS], pos[STEPS], blk[STEPS], b0[STEPS], b1[STEPS];
-    bool fresh[STEPS];  // the first block is a new one
+    int32_t kk[STEPS], pos[STEPS], blk[STEPS];
+    Vec<int32_t, 2> b[STEPS];
 #pragma unroll
     for (int u = 0; u < STEPS; ++u) {
       const int i = (u * BWG + tid) * 2;
-      const int k = s.req[i], kn = min(k, kNear - 1);
-      const int64_t at64 = s.pos0[kn] + i, free0 = s.free0[kn];
-      const int32_t have = s.have[kn];
-      const bool pair = i + 2 <= cnt && k == s.req[i + 1] && k < kNear && a.bs >= 2 && at64 >= 0 &&
-                        at64 < INT32_MAX;
-      kk[u] = pair ? k : -1;
-      pos[u] = pair ? (int32_t)at64 : 0;
+      const int2 k = *(const int2 *)&s.req[i];
+      const Near q = s.near[min(k.x, kNear - 1)];
+      pos[u] = q.pos0 + i;
       blk[u] = block_of(a, pos[u]);
-      fresh[u] = blk[u] >= have;
-      const int32_t *p0 = pair ? look(k, blk[u], free0, have) : nullptr;
-      const int32_t *p1 = pair ? look(k, blk[u] + 1, free0, have) : nullptr;
-      b0[u] = *(p0 ? p0 : none);
-      b1[u] = *(p1 ? p1 : none);
-      b0[u] = p0 ? b0[u] : -1;
-      b1[u] = p1 ? b1[u] : -1;
+      const int64_t f = q.free0 + blk[u];
+      const bool pair = i + 2 <= cnt && k.x == k.y && k.x < kNear && blk[u] >= q.have &&
+                        blk[u] + 1 < a.width && f + 1 < a.n_free;
+      kk[u] = pair ? k.x : -1;
+      b[u] = load_vec<int32_t, 2>(pair ? a.free_blocks + f : (const int32_t *)a.off);
       if (!pair && i < cnt) s.slow[atomicAdd(&s.n_slow, 1)] = (int16_t)i;
     }
 #pragma unroll
@@ -240,12 +253,13 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
       const int i = (u * BWG + tid) * 2;
       const int32_t at = pos[u] - blk[u] * a.bs;
       const bool two = at + 1 == a.bs;
-      if (at == 0 && fresh[u]) enter(kk[u], blk[u], b0[u]);
-      // (the second block's first place is a new token's: it is a new block)
-      if (two) enter(kk[u], blk[u] + 1, b1[u]);
-      if (blk[u] + two >= a.width) status |= BPE_STATUS_TABLE_FULL;
-      const bool ok0 = b0[u] >= 0 && blk[u] < a.width, ok1 = b1[u] >= 0 && blk[u] + 1 < a.width;
-      const int64_t s0 = (int64_t)b0[u] * a.bs + at, s1 = (int64_t)b1[u] * a.bs;
+      if (at == 0 || two) {  // a block's first token enters it
+        int32_t *entry = a.table + (r0 + kk[u]) * a.stride + blk[u];
+        if (at == 0) entry[0] = b[u].v[0];
+        if (two) entry[1] = b[u].v[1];
+      }
+      const int64_t s0 = (int64_t)b[u].v[0] * a.bs + at, s1 = (int64_t)b[u].v[1] * a.bs;
+      const bool ok0 = b[u].v[0] >= 0, ok1 = b[u].v[1] >= 0;
       Vec<int64_t, 2> slot;
       Vec<int32_t, 2> posn;
       slot.v[0] = ok0 ? s0 : -1;
@@ -253,34 +267,31 @@ __global__ void __launch_bounds__(BWG) k_block_fill(BlockArgs a) {
       posn.v[0] = pos[u];
       posn.v[1] = pos[u] + 1;
       store_vec<int64_t, 2, STREAM>(a.slots + i0 + i, slot);
-      store_vec<int32_t, 2, STREAM>(a.positions + i0 + i, posn);
+      store_vec(a.positions + i0 + i, posn);
     }
     __syncthreads();
-    // the others one by one, side by side
+    // the other tokens one by one, side by side
     for (int j = tid; j < s.n_slow * 2; j += BWG) {
       const int i = s.slow[j >> 1] + (j & 1);
       if (i >= cnt) continue;
-      const int k = s.req[i];
-      int64_t at64, free0;
+      const int64_t r = r0 + s.req[i];
+      int64_t at64, free0, slot = -1;
       int32_t have, position = -1;
-      int64_t slot = -1;
-      if (k < kNear) {
-        at64 = s.pos0[k];
-        free0 = s.free0[k];
-        have = s.have[k];
-      } else {
-        const int64_t r = r0 + k;
-        place(r, a.off[r], a.cached[r], FUSED ? 0 : a.first[r], &at64, &free0, &have);
-      }
+      place(r, a.off[r], a.cached[r], FUSED ? 0 : a.first[r], &at64, &free0, &have);
       at64 += i;
       if (at64 >= 0 && at64 <= INT32_MAX) {
         position = (int32_t)at64;
         const int32_t bk = block_of(a, position), at = position - bk * a.bs;
-        const int32_t *p = look(k, bk, free0, have);
-        const int32_t block = p ? *p : -1;
-        if (at == 0 && bk >= have) enter(k, bk, block);
-        if (bk >= a.width) status |= BPE_STATUS_TABLE_FULL;
-        else if (block >= 0) slot = (int64_t)block * a.bs + at;
+        if (bk >= a.width) {
+          status |= BPE_STATUS_TABLE_FULL;
+        } else {
+          int32_t *entry = a.table + r * a.stride + bk;
+          int32_t block = -1;
+          if (bk < have) block = *entry;
+          else if (free0 + bk < a.n_free) block = a.free_blocks[free0 + bk];
+          if (bk >= have && at == 0) *entry = block;
+          if (block >= 0) slot = (int64_t)block * a.bs + at;
+        }
       }
       a.slots[i0 + i] = slot;
       a.positions[i0 + i] = position;

@@ -40,7 +40,10 @@ hipError_t launch_embed(const EmbedArgs &a, int wt, int ot, hipStream_t stream);
 constexpr int kEmbedUnits = 1024;  // vectors per workgroup of the forward
 constexpr int kZeroRows = 16;      // rows of the table per workgroup of zeros
 constexpr int kGradTile = 256;     // IDs per tile of the sums, at most
-constexpr int kGradDirect = 2048;  // IDs up to which no sort is made
+constexpr int kDirectWG = 512;
+constexpr int kGradDirect = 4 * kDirectWG;  // IDs up to which no sort is made
+constexpr int kGradSmall = 6144;            // IDs that one workgroup sorts,
+constexpr int64_t kGradSmallRows = 1 << 20; // and rows whose marks it clears
 constexpr int kDigitBits = 9;
 constexpr int kMaxDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 512;
@@ -91,7 +94,7 @@ struct BlockArgs {
   int32_t *table;
   int64_t width, stride;
   int32_t bs;
-  uint32_t magic;     // x / bs = (x * magic) >> shift for 0 <= x < 2^31
+  uint32_t magic;     // x / bs = mulhi(x, magic) >> shift for 0 <= x < 2^31, bs > 1
   int32_t shift;
   int64_t *slots;
   int32_t *positions, *lengths;

@@ -47,14 +47,14 @@ __device__ __forceinline__ Vec<int32_t, 4> load_ids(const int32_t *p, int64_t i,
 // vocab words exist in memory.  Left in step 3, the divisions and searches of
 // step 2 are executed for nearly every vector of a wave for one lane's sake.
 template <typename TI, typename TO, int NT, bool STREAM>
-__global__ void __launch_bounds__(NT) k_logits(bpe_logits_args a) {
+__global__ void __launch_bounds__(NT, 8) k_logits(bpe_logits_args a) {
   constexpr int S = NT * kLogitPer;
   constexpr int E = 4;             // logits per vector: 16 bytes of float32
   constexpr int U = S / (NT * E);  // vectors per thread
   constexpr int LU = 4, STEP = NT * 4;  // list loads in flight, IDs per step
   __shared__ __align__(16) uint32_t tab[S];
   __shared__ __align__(16) uint32_t done[S / 32];
-  constexpr int Q = S / 4;         // places in the queue
+  constexpr int Q = S / 8;         // places in the queue
   __shared__ uint16_t queue[Q];
   __shared__ float biases[kBiasSlots];
   __shared__ int32_t queued;
