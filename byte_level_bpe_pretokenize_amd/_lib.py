@@ -32,7 +32,7 @@ STATUS_BAD_DOC_OFFSETS, STATUS_IDS_CAPACITY, STATUS_BAD_ID, STATUS_BYTES_CAPACIT
 STATUS_NO_BLOCKS, STATUS_TABLE_FULL, STATUS_BAD_LENGTH, STATUS_BAD_MASK_ROW, STATUS_BAD_BIAS = \
     32, 64, 128, 256, 512
 F32, BF16, F16 = 0, 1, 2
-MAX_WIDTH = 1 << 18
+MAX_WIDTH = 1 << 17
 MAX_ROWS = 1 << 26
 OP_ENCODE, OP_DECODE = 0, 1
 MAX_MERGES = 1 << 20

@@ -121,6 +121,7 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
   if (n_ids > kGradDirect) {
     const GradLayout L = grad_layout(n_ids, n_rows, width);
     if (workspace_bytes < L.total) return BPE_EWORKSPACE;
+    if ((uintptr_t)d_workspace & 15) return BPE_EINVAL;
     uint8_t *ws = (uint8_t *)d_workspace;
     a.key[0] = (int32_t *)(ws + L.key0);
     a.key[1] = (int32_t *)(ws + L.key1);
@@ -221,6 +222,7 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
   a.used = d_used;
   a.status = d_status;
   if (n_requests > kBlockFused) {
+    if ((uintptr_t)d_workspace & 7) return BPE_EINVAL;
     a.first = (int64_t *)d_workspace;
     a.gsum = a.first + n_requests;
     a.chunk_req = (int32_t *)(a.gsum + kBlockGroups);

@@ -51,7 +51,7 @@ extern "C" {
 #define BPE_STATUS_BAD_BIAS 512u     /* a row's bias IDs do not increase */
 
 /* limits */
-#define BPE_MAX_WIDTH (1 << 18)             /* columns of an embedding table */
+#define BPE_MAX_WIDTH (1 << 17)             /* columns of an embedding table */
 #define BPE_MAX_ROWS ((int64_t)1 << 26)     /* rows of an embedding table, columns of logits */
 #define BPE_MAX_IDS ((int64_t)1 << 30)      /* IDs per embedding call */
 
@@ -68,7 +68,8 @@ int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t wid
               int32_t pad_id, void *d_out, int out_type, int64_t out_stride, int32_t *d_status,
               void *hip_stream);
 
-/* Workspace bytes bpe_embed_grad needs (0 for n_ids <= 0 or a size out of range). */
+/* Workspace bytes bpe_embed_grad needs (0 for few IDs and for a size out of
+ * range). */
 size_t bpe_embed_grad_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t width);
 
 /*
@@ -80,8 +81,9 @@ size_t bpe_embed_grad_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t wid
  *            IDs that do not occur are neither read nor written.
  * Positions whose ID is pad_id add nothing; so do IDs outside [0, n_rows),
  * which set BPE_STATUS_BAD_ID.  Each row's terms are added in float32 in an
- * order that the IDs alone fix.  d_workspace: device scratch of
- * workspace_bytes >= bpe_embed_grad_workspace_bytes(n_ids, n_rows, width).
+ * order that the IDs alone fix.  d_workspace: device scratch, 16-byte aligned,
+ * of workspace_bytes >= bpe_embed_grad_workspace_bytes(n_ids, n_rows, width)
+ * (NULL where that is 0).
  * Returns BPE_OK, BPE_EINVAL, BPE_EWORKSPACE or BPE_EHIP.
  */
 int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const int32_t *d_ids,

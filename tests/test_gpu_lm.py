@@ -62,7 +62,7 @@ def status():
 @pytest.mark.parametrize("wt,ot", [(BF16, BF16), (F32, BF16), (F32, F32), (F16, F16), (BF16, F32),
                                    (F16, BF16), (F32, F16)])
 @pytest.mark.parametrize("n,V,D", [(1, 1, 1), (2, 5, 3), (65, 768, 7), (64, 300, 8), (33, 300, 9),
-                                   (1000, 50, 64), (130, 1000, 513), (17, 40, 4096), (3, 9, 8191)])
+                                   (1000, 50, 64), (130, 1000, 513), (17, 40, 4096), (3, 9, 8191), (3, 2, 1 << 17), (2, 2, (1 << 17) - 1)])
 def test_embed(n, V, D, wt, ot):
     w = randn((V, D), wt, 1)
     ids = ids_of(n, V, n)
@@ -534,7 +534,7 @@ def test_blocks_bad_lengths_and_offsets(R):
     assert torch.all(pos[int(off[1]) + 2:int(off[2])] == -1)
     # offsets that are not valid: the bit, and nothing out of bounds (guards around every output)
     T = int(off[-1])
-    for at, v in ((0, 3), (R, T - 1), (R, T + 5), (3, -7), (2, 10**15), (R // 2, -10**15)):
+    for at, v in ((0, 3), (R, T - 1), (R, T + 5), (3, -7), (2, 10**15), (R // 2, -10**15), (1, 2**63 - 1), (R - 1, -2**63)):
         o = off.copy()
         o[at] = v
         guard = 64

@@ -36,8 +36,10 @@ def test_header_constants():
                         ("BPE_STATUS_BAD_LENGTH", _lib.STATUS_BAD_LENGTH),
                         ("BPE_STATUS_BAD_MASK_ROW", _lib.STATUS_BAD_MASK_ROW),
                         ("BPE_STATUS_BAD_BIAS", _lib.STATUS_BAD_BIAS),
+                        ("BPE_MAX_WIDTH", f"(1 << {_lib.MAX_WIDTH.bit_length() - 1})"),
+                        ("BPE_MAX_ROWS", f"((int64_t)1 << {_lib.MAX_ROWS.bit_length() - 1})"),
                         ("BPE_F32", _lib.F32), ("BPE_BF16", _lib.BF16), ("BPE_F16", _lib.F16)):
-        assert re.search(rf"#define {name} {value}u?\b", header()), name
+        assert re.search(rf"#define {name} {re.escape(str(value))}u?\s", header()), name
 
 
 def embed_rc(weight=P, wt=0, V=100, D=64, ws=64, ids=P, n=5, scale=1.0, pad=-1, out=P, ot=0, os_=64,
@@ -49,7 +51,7 @@ def embed_rc(weight=P, wt=0, V=100, D=64, ws=64, ids=P, n=5, scale=1.0, pad=-1, 
     dict(weight=None), dict(ids=None), dict(out=None), dict(status=None), dict(wt=3), dict(ot=-1),
     dict(V=0), dict(V=_lib.MAX_ROWS + 1), dict(D=0), dict(D=_lib.MAX_WIDTH + 1, ws=1 << 20, os_=1 << 20),
     dict(ws=63), dict(os_=63), dict(n=-1), dict(n=(1 << 30) + 1), dict(pad=-2),
-    dict(ws=(1 << 32) + 1), dict(n=1 << 30, D=1 << 18, ws=1 << 18, os_=1 << 18),
+    dict(ws=(1 << 32) + 1), dict(n=1 << 30, D=1 << 17, ws=1 << 17, os_=1 << 17),
 ])
 def test_embed_refuses(bad):
     assert embed_rc(**bad) == _lib.BPE_EINVAL
@@ -68,9 +70,9 @@ def grad_rc(grad=P, gt=1, gs=64, ids=P, n=5000, V=100, D=64, scale=1.0, pad=-1, 
 
 
 @pytest.mark.parametrize("bad", [
-    dict(grad=None), dict(ids=None), dict(out=None), dict(status=None), dict(ws=None), dict(gt=7),
+    dict(grad=None), dict(ids=None), dict(out=None), dict(status=None), dict(ws=None), dict(ws=P + 8), dict(gt=7),
     dict(ot=9), dict(V=0), dict(D=0), dict(D=_lib.MAX_WIDTH + 1, gs=1 << 20, os_=1 << 20), dict(gs=63),
-    dict(os_=63), dict(n=-1), dict(pad=-2), dict(n=1 << 30, D=1 << 18, gs=1 << 18, os_=1 << 18),
+    dict(os_=63), dict(n=-1), dict(pad=-2), dict(n=1 << 30, D=1 << 17, gs=1 << 17, os_=1 << 17),
 ])
 def test_embed_grad_refuses(bad):
     assert grad_rc(**bad) == _lib.BPE_EINVAL
@@ -125,7 +127,7 @@ def blocks_rc(off=P, R=3, T=10, cached=P, free=P, n_free=5, table=P, W=4, stride
 
 @pytest.mark.parametrize("bad", [
     dict(off=None), dict(cached=None), dict(free=None), dict(table=None), dict(slots=None),
-    dict(positions=None), dict(lengths=None), dict(used=None), dict(ws=None, R=5000), dict(status=None),
+    dict(positions=None), dict(lengths=None), dict(used=None), dict(ws=None, R=5000), dict(ws=P + 4, R=5000), dict(status=None),
     dict(R=-1), dict(T=-1), dict(n_free=-1), dict(W=-1), dict(W=1 << 31, stride=1 << 31),
     dict(stride=3), dict(bs=0), dict(bs=-4), dict(R=0), dict(T=1 << 35), dict(R=(1 << 30) + 1),
 ])
@@ -208,6 +210,32 @@ def test_binding_refuses(error, call):
 def test_binding_needs_a_gpu():
     with pytest.raises(RuntimeError, match="HIP device"):
         lm.embed(z(4, 8), z(3, dtype=I32))
+
+
+# ---- the divisions by multiplication that the kernels use -------------------------
+@pytest.mark.parametrize("units", [1, 2, 3, 7, 125, 126, 512, 4095, 16385, 32767, 32768])
+def test_division_of_vectors(units):
+    """x / units = mulhi(2 x, 2^31 / units + 1) for a workgroup's x < units + 1024,
+    up to the widest table's vectors of 4."""
+    assert units <= (_lib.MAX_WIDTH + 3) // 4
+    magic = (1 << 31) // units + 1
+    x = np.arange(units + 1024, dtype=np.uint64)
+    assert magic < 1 << 32 and int(x[-1]) * units < 1 << 31
+    assert np.array_equal((2 * x * np.uint64(magic)) >> np.uint64(32), x // np.uint64(units))
+
+
+@pytest.mark.parametrize("bs", [2, 3, 7, 16, 48, 1000, (1 << 20) - 3, (1 << 30) + 1, (1 << 31) - 1])
+def test_division_by_the_block_size(bs):
+    """x / bs = mulhi(x, 2^(31 + s) / bs + 1) >> (s - 1), 2^s >= bs, for x < 2^31."""
+    s = (bs - 1).bit_length()
+    magic = (1 << (31 + s)) // bs + 1
+    assert magic < 1 << 32
+    rng = np.random.default_rng(bs)
+    x = np.concatenate([np.arange(5000), (1 << 31) - 1 - np.arange(5000), rng.integers(0, 1 << 31, 20000),
+                        np.minimum(bs * rng.integers(0, (1 << 31) // bs + 1, 5000), (1 << 31) - 1),
+                        np.clip(bs * rng.integers(0, (1 << 31) // bs + 1, 5000) - 1, 0, (1 << 31) - 1)])
+    for v in x.tolist():
+        assert (v * magic >> 32) >> (s - 1) == v // bs
 
 
 # ---- the references against the definitions, by hand ------------------------------
