@@ -172,7 +172,7 @@ int bpe_process_logits(const bpe_logits_args *args, void *hip_stream) {
     return BPE_EINVAL;
   if (a.mask && !stride_ok(a.mask_stride, (a.vocab + 31) / 32)) return BPE_EINVAL;
   if (!any) return BPE_OK;
-  if ((a.vocab / (256 * kLogitPer) + 1) * a.rows > kMaxGrid) return BPE_EINVAL;
+  if ((a.vocab / kLogitSlab + 1) * a.rows > kMaxGrid) return BPE_EINVAL;
   return launch_logits(a, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }
 

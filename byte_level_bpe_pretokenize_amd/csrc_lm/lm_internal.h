@@ -81,7 +81,7 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width);
 hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);
 
 // ---- logits ------------------------------------------------------------------
-constexpr int kLogitPer = 16;  // logits per thread
+constexpr int kLogitSlab = 4096;  // logits per workgroup, at least
 
 hipError_t launch_logits(const bpe_logits_args &a, hipStream_t stream);
 

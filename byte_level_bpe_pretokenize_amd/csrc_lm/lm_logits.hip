@@ -45,10 +45,14 @@ __device__ __forceinline__ Vec<int32_t, 4> load_ids(const int32_t *p, int64_t i,
 //    them.
 // A row's lists are read once per slab (from L2), so that no counts of rows *
 // vocab words exist in memory.  Left in step 3, the divisions and searches of
-// step 2 are executed for nearly every vector of a wave for one lane's sake.
-template <typename TI, typename TO, int NT, bool STREAM>
+// step 2 are executed for nearly every vector of a wave for one lane's sake
+// (80 us instead of 40).  Lists that do not fit one step of the workgroup have
+// no queue: every word is looked at instead.
+// Bound by memory with short lists: 256 rows of 128,256 bfloat16 logits to
+// float32, 198 MB, take 39 us, 5.0 TB/s (a plain conversion 30 us).  Bound by
+// the longest list with long ones: its IDs are read by one workgroup per slab.
+template <typename TI, typename TO, int NT, int S, bool STREAM>
 __global__ void __launch_bounds__(NT, 8) k_logits(bpe_logits_args a) {
-  constexpr int S = NT * kLogitPer;
   constexpr int E = 4;             // logits per vector: 16 bytes of float32
   constexpr int U = S / (NT * E);  // vectors per thread
   constexpr int LU = 4, STEP = NT * 4;  // list loads in flight, IDs per step
@@ -168,11 +172,16 @@ __global__ void __launch_bounds__(NT, 8) k_logits(bpe_logits_args a) {
   if (tid * 4 < np) count(p0, tid * 4, np, true);
   if (tid * 4 < made) count(m0, tid * 4, made, false);
   if (tid < nb) bias(bv, bprev, bval, tid);
-  for (int64_t i = STEP + tid * 4; i < np; i += STEP * LU) {
+  int64_t from = STEP;
+  for (; from + STEP * LU <= np; from += STEP * LU) {
     Vec<int32_t, 4> y[LU];
 #pragma unroll
-    for (int l = 0; l < LU; ++l) y[l] = load_ids(pp, i + l * STEP, np);
-    count_only(y, i, np, true);
+    for (int l = 0; l < LU; ++l) y[l] = load_vec<int32_t, 4>(pp + from + l * STEP + tid * 4);
+    count_only(y, from + tid * 4, np, true);
+  }
+  for (; from < np; from += STEP) {
+    const Vec<int32_t, 4> y[1] = {load_ids(pp, from + tid * 4, np)};
+    count_only(y, from + tid * 4, np, true);
   }
   for (int64_t i = STEP + tid * 4; i < made; i += STEP) {
     const Vec<int32_t, 4> y[1] = {load_ids(mp, i, made)};
@@ -272,23 +281,22 @@ __global__ void __launch_bounds__(NT, 8) k_logits(bpe_logits_args a) {
   }
 }
 
-template <typename TI, typename TO, int NT, bool STREAM>
+template <typename TI, typename TO, int NT, int S, bool STREAM>
 hipError_t logits_launch(const bpe_logits_args &a, hipStream_t stream) {
-  constexpr int S = NT * kLogitPer;
-  hipLaunchKernelGGL((k_logits<TI, TO, NT, STREAM>),
+  hipLaunchKernelGGL((k_logits<TI, TO, NT, S, STREAM>),
                      dim3((unsigned)((a.vocab + S - 1) / S * a.rows)), dim3(NT), 0, stream, a);
   return hipGetLastError();
 }
 
 // Long lists are read by wide workgroups, in half as many slabs (24 rows of
-// 100,256 logits with 26,000 prompt IDs each: 20 us with 512 threads, 26 with
+// 100,256 logits with 26,000 prompt IDs each: 18 us with 1024 threads, 26 with
 // 256); short ones leave narrow workgroups ahead (256 rows of 128,256 with 600:
-// 46 and 42 us).
+// 75 and 39 us).
 template <typename TI, typename TO, bool STREAM>
 hipError_t logits_wide(const bpe_logits_args &a, hipStream_t stream) {
   const bool longer = a.n_prompt / a.rows + a.made_width > 4096;
-  return longer ? logits_launch<TI, TO, 512, STREAM>(a, stream)
-                : logits_launch<TI, TO, 256, STREAM>(a, stream);
+  return longer ? logits_launch<TI, TO, 1024, 2 * kLogitSlab, STREAM>(a, stream)
+                : logits_launch<TI, TO, 256, kLogitSlab, STREAM>(a, stream);
 }
 
 template <typename TI, typename TO>

@@ -326,8 +326,9 @@ def test_logits_in_place_and_strided(V):
 
 
 def test_logits_long_history():
-    x, args, want, tol = logits_case(3, 20000, F32, 5, prompt=30000, made=5000, bias=300)
-    ref.check(lm.process_logits(x, **args), want, tol)
+    for lt, V in ((F32, 20000), (BF16, 8192), (BF16, 24577)):
+        x, args, want, tol = logits_case(3, V, lt, 5, prompt=30000, made=5000, bias=300)
+        ref.check(lm.process_logits(x, **args), want, tol)
 
 
 @pytest.mark.parametrize("bias", [512, 513, 900, 4000])
