@@ -20,7 +20,7 @@ SYMBOLS = (
 
 # every symbol include/bpe_lm.h declares
 LM_SYMBOLS = (
-    "bpe_embed", "bpe_embed_grad_workspace_bytes", "bpe_embed_grad", "bpe_process_logits",
+    "bpe_embed_workspace_bytes", "bpe_embed", "bpe_embed_grad_workspace_bytes", "bpe_embed_grad", "bpe_process_logits",
     "bpe_block_tables_workspace_bytes", "bpe_block_tables",
 )
 
@@ -112,7 +112,9 @@ def load() -> C.CDLL:
     L.bpe_strerror.argtypes = [i32]
     L.bpe_strerror.restype = C.c_char_p
     f32 = C.c_float
-    L.bpe_embed.argtypes = [p, i32, i64, i64, i64, p, i64, f32, i32, p, i32, i64, p, p]
+    L.bpe_embed_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    L.bpe_embed_workspace_bytes.restype = sz
+    L.bpe_embed.argtypes = [p, i32, i64, i64, i64, p, i64, f32, i32, p, i32, i64, p, sz, p, p]
     L.bpe_embed.restype = i32
     L.bpe_embed_grad_workspace_bytes.argtypes = [i64, i64, i64]
     L.bpe_embed_grad_workspace_bytes.restype = sz

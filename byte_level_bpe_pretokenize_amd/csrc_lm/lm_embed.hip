@@ -17,8 +17,9 @@ namespace {
 // without, 659 with).
 // Bound by memory: those 2.57 GB (each row of the table read once) move at 3.9
 // TB/s, where a copy of 8 GiB makes 4.7; what is missing are rows that fell out
-// of the caches and are read again.  Column slabs, one per XCD or one after
-// another, keep more rows in the caches but store shorter runs: 648 to 788 us.
+// of the L2s and are read again (2.6 GB instead of 0.4).  Column slabs, one per
+// XCD or one after another, keep more rows in the caches but store shorter
+// runs: 648 to 788 us.
 // 64 IDs take 3.2 us.
 template <typename TI, typename TO, int E, int U, bool BIG>
 __global__ void __launch_bounds__(256) k_embed(EmbedArgs a) {
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_count(GradArgs a, int pas
   const int tid = threadIdx.x, digits = 1 << a.bits;
   const int64_t i0 = (int64_t)blockIdx.x * kSortTile;
   for (int d = tid; d < digits; d += kSortThreads) cnt[d] = 0;
-  if (pass == 0)
+  if (pass == 0 && a.touched)
     for (int64_t v = (int64_t)blockIdx.x * kSortThreads + tid; v < a.n_rows;
          v += (int64_t)gridDim.x * kSortThreads)
       a.touched[v] = 0;
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_scatter(GradArgs a, int p
     if (!place_key(key[j], shift, a.bits, base[wv], &at)) continue;
     a.key[pass & 1][at] = key[j];
     a.pos[pass & 1][at] = pos[j];
-    if (last && key[j] < a.n_rows) a.touched[key[j]] = 1;
+    if (last && a.touched && key[j] < a.n_rows) a.touched[key[j]] = 1;
   }
 }
 
@@ -244,6 +245,66 @@ __global__ void __launch_bounds__(kGradSmall / 8) k_grad_sort(GradArgs a) {
       key[j] = i < n ? keys[i] : -1;
       pos[j] = i < n ? places[i] : 0;
     }
+  }
+}
+
+// ---- forward, by sorted IDs ------------------------------------------------------
+// The same rows in the order of their IDs: one wave per 64 positions of the
+// sorted list and 64 vectors of columns loads a row of the table once and
+// stores it to all of its positions.  kRunAhead positions' rows are loaded
+// before the last ones are stored.  Bound by the stores, whose rows lie in no
+// order: the 262,144 IDs of above take 540 us after 30 for the sort (1, 4, 8 or
+// 16 waves per workgroup, stored past the caches or not: the same).
+constexpr int kRunAhead = 4;
+
+template <typename TI, typename TO, int E>
+__global__ void __launch_bounds__(256) k_embed_runs(EmbedArgs a) {
+  const int lane = lane_id();
+  const int64_t w = (int64_t)blockIdx.x * 4 + uniform_wave_id();
+  const int64_t tile = w / a.slabs;
+  const int slab = (int)(w - tile * a.slabs);
+  const int64_t i0 = tile * 64;
+  if (i0 >= a.n_ids) return;
+  const int n = (int)min<int64_t>(64, a.n_ids - i0);
+  const int c = (slab * 64 + lane) * E, col = min(c, a.width - E);
+  const bool mine = c < a.width;
+  const int32_t key = a.key[i0 + min(lane, n - 1)], pos = a.pos[i0 + min(lane, n - 1)];
+  const int32_t none = (int32_t)a.n_rows;
+  Vec<TI, E> x[2][kRunAhead];
+  Vec<TO, E> r;
+  int32_t cur = -1;
+  // (each row's first position loads it; every lane stays active around the
+  // lane reads)
+  auto fetch = [&](Vec<TI, E> (&y)[kRunAhead], int at) {
+#pragma unroll
+    for (int j = 0; j < kRunAhead; ++j) {
+      const int i = min(at + j, n - 1);
+      const int32_t k = lane_value(key, i);
+      if (k != none && (i == 0 || k != lane_value(key, i - 1)))
+        y[j] = load_vec<TI, E>((const TI *)a.weight + k * a.w_stride + col);
+    }
+  };
+  auto put = [&](Vec<TI, E> (&y)[kRunAhead], int at) {
+#pragma unroll
+    for (int j = 0; j < kRunAhead; ++j) {
+      if (at + j >= n) break;
+      const int32_t k = lane_value(key, at + j);
+      if (k != cur) {
+        cur = k;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          r.v[e] = from_f32<TO>(k != none ? (float)y[j].v[e] * a.scale : 0.f);
+      }
+      if (mine)
+        store_vec<TO, E, true>((TO *)a.out + (int64_t)lane_value(pos, at + j) * a.o_stride + col, r);
+    }
+  };
+  fetch(x[0], 0);
+  for (int b = 0; b < n; b += 2 * kRunAhead) {
+    if (b + kRunAhead < n) fetch(x[1], b + kRunAhead);
+    put(x[0], b);
+    if (b + 2 * kRunAhead < n) fetch(x[0], b + 2 * kRunAhead);
+    if (b + kRunAhead < n) put(x[1], b + kRunAhead);
   }
 }
 
@@ -603,11 +664,25 @@ hipError_t embed_as(EmbedArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+void launch_sort(const GradArgs &a, hipStream_t stream) {
+  for (int pass = 0; pass < a.passes; ++pass) {
+    hipLaunchKernelGGL(k_grad_count, dim3(a.sort_tiles), dim3(kSortThreads), 0, stream, a, pass);
+    hipLaunchKernelGGL(k_grad_scatter, dim3(a.sort_tiles), dim3(kSortThreads), 0, stream, a, pass);
+  }
+}
+
 template <typename TI, typename TO>
-hipError_t embed_of(const EmbedArgs &a, hipStream_t stream) {
+hipError_t embed_of(EmbedArgs a, hipStream_t stream) {
   if (a.width < 8) return embed_as<TI, TO, 1, false>(a, stream);
   const bool big = a.n_ids * a.width * (int64_t)sizeof(TO) >= kStreamBytes;
   constexpr int E = 16 / sizeof(TO);
+  if (a.key) {
+    a.slabs = (a.width + 64 * E - 1) / (64 * E);
+    const int64_t waves = (a.n_ids + 63) / 64 * a.slabs;
+    hipLaunchKernelGGL((k_embed_runs<TI, TO, E>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0,
+                       stream, a);
+    return hipGetLastError();
+  }
   return big ? embed_as<TI, TO, E, true>(a, stream) : embed_as<TI, TO, E, false>(a, stream);
 }
 
@@ -631,10 +706,7 @@ hipError_t grad_as(GradArgs a, hipStream_t stream) {
   const bool small = a.n_ids <= kGradSmall && a.n_rows <= kGradSmallRows;
   if (a.n_ids > 0 && small)
     hipLaunchKernelGGL(k_grad_sort, dim3(1), dim3(kGradSmall / 8), 0, stream, a);
-  for (int pass = 0; a.n_ids > 0 && !small && pass < a.passes; ++pass) {
-    hipLaunchKernelGGL(k_grad_count, dim3(a.sort_tiles), dim3(kSortThreads), 0, stream, a, pass);
-    hipLaunchKernelGGL(k_grad_scatter, dim3(a.sort_tiles), dim3(kSortThreads), 0, stream, a, pass);
-  }
+  if (a.n_ids > 0 && !small) launch_sort(a, stream);
   a.sum_blocks = a.n_ids > 0 ? ((int64_t)a.tiles * a.slabs + 3) / 4 : 0;
   const int64_t zero = a.accumulate ? 0 : (a.n_rows + kZeroRows - 1) / kZeroRows;
   if (a.sum_blocks + zero > 0)
@@ -662,7 +734,9 @@ hipError_t grad_from(const GradArgs &a, int ot, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_embed(const EmbedArgs &a, int wt, int ot, hipStream_t stream) {
+hipError_t launch_embed(const EmbedArgs &a, const GradArgs *sort, int wt, int ot,
+                        hipStream_t stream) {
+  if (sort) launch_sort(*sort, stream);
   if (wt == BPE_F32) return embed_from<float>(a, ot, stream);
   if (wt == BPE_BF16) return embed_from<bf16_t>(a, ot, stream);
   return embed_from<f16_t>(a, ot, stream);

@@ -27,11 +27,11 @@ struct EmbedArgs {
   int32_t width;
   int32_t pad_id;
   float scale;
-  uint32_t units;   // vectors per row and slab
+  uint32_t units;   // vectors per row
   uint32_t magic;   // 2^31 / units + 1: x / units = x * magic >> 31 while x * units < 2^31
+  const int32_t *key, *pos;  // the sorted IDs and their positions, or nullptr
+  int32_t slabs;             // column groups of 64 vectors
 };
-
-hipError_t launch_embed(const EmbedArgs &a, int wt, int ot, hipStream_t stream);
 
 // ---- the embedding's gradient ----------------------------------------------
 // The IDs are sorted (a stable radix sort of at most kDigitBits bits per pass,
@@ -62,7 +62,7 @@ struct GradArgs {
   // workspace
   int32_t *key[2], *pos[2];  // sorted IDs (n_rows: adds nothing) and their positions
   int32_t *counts;           // [sort tiles][digits]
-  uint8_t *touched;          // [n_rows] 1: the ID occurs
+  uint8_t *touched;          // [n_rows] 1: the ID occurs; or nullptr
   float *part;               // [tiles][2][width] sums of rows that a tile's edge cuts
   // launch
   int32_t sort_tiles, passes, bits;  // bits of one pass's digit
@@ -76,6 +76,10 @@ struct GradLayout {
   size_t key0, key1, pos0, pos1, counts, touched, part, total;
   int32_t sort_tiles, passes, bits, tile, tiles;
 };
+
+// a.key != nullptr: by sorted IDs, after the sort that `sort` describes.
+hipError_t launch_embed(const EmbedArgs &a, const GradArgs *sort, int wt, int ot,
+                        hipStream_t stream);
 
 GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width);
 hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);

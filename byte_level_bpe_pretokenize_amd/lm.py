@@ -120,17 +120,25 @@ def _on(stream, call, tensors, *args, **kw):
     return res
 
 
+def embed_workspace_bytes(n_ids: int, n_rows: int, width: int, weight_dtype: torch.dtype,
+                          out_dtype: torch.dtype) -> int:
+    return int(_lib.load().bpe_embed_workspace_bytes(
+        n_ids, n_rows, width, _type(weight_dtype, "weight_dtype"), _type(out_dtype, "out_dtype")))
+
+
 def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id: int = -1,
           out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
-          status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+          workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+          stream=None) -> torch.Tensor:
     """bpe_embed: ``scale * weight[ids]``, zeros where an ID is ``pad_id``.
 
     weight (V, D); ids int32, contiguous, any shape; returns ids.shape + (D,)
     of ``out_dtype`` (the weight's by default), or ``out``, a matrix of
-    ids.numel() rows, filled."""
+    ids.numel() rows, filled.  ``workspace``: a contiguous device tensor of
+    embed_workspace_bytes bytes, allocated by the call when left out."""
     if stream is not None:
-        return _on(stream, embed, (weight, ids, out, status), weight, ids, scale, pad_id=pad_id,
-                   out=out, out_dtype=out_dtype, status=status)
+        return _on(stream, embed, (weight, ids, out, workspace, status), weight, ids, scale,
+                   pad_id=pad_id, out=out, out_dtype=out_dtype, workspace=workspace, status=status)
     pad_id = _int32(pad_id, -1, "pad_id")
     wt = _type(weight.dtype, "weight")
     ws = _rows(weight, "weight")
@@ -143,11 +151,22 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
         ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
         if tuple(out.shape) != (n, D) or out_dtype not in (None, out.dtype):
             raise ValueError(f"out: ({n}, {D}) of out_dtype expected, got {tuple(out.shape)}")
-    dev = _device("embed", (weight, ids, out, status))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    dev = _device("embed", (weight, ids, out, workspace, status))
+    L = _lib.load()
     st = _status(status, dev)
     res = torch.empty((*ids.shape, D), dtype=dt, device=dev) if out is None else out
-    rc = _lib.load().bpe_embed(weight.data_ptr(), wt, V, D, ws, ip, n, scale, pad_id,
-                               res.data_ptr(), ot, os_, st.data_ptr(), _stream(dev))
+    w_ptr, w_bytes = None, 0
+    if workspace is not None:
+        w_ptr, w_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif n > V:  # (fewer IDs never need one)
+        w_bytes = L.bpe_embed_workspace_bytes(n, V, D, wt, ot)
+        if w_bytes:
+            workspace = torch.empty(w_bytes, dtype=torch.uint8, device=dev)
+            w_ptr = workspace.data_ptr()
+    rc = L.bpe_embed(weight.data_ptr(), wt, V, D, ws, ip, n, scale, pad_id, res.data_ptr(), ot,
+                     os_, w_ptr, w_bytes, st.data_ptr(), _stream(dev))
     _end("bpe_embed", rc, st if status is None else None)
     return res
 

@@ -55,18 +55,26 @@ extern "C" {
 #define BPE_MAX_ROWS ((int64_t)1 << 26)     /* rows of an embedding table, columns of logits */
 #define BPE_MAX_IDS ((int64_t)1 << 30)      /* IDs per embedding call */
 
+/* Workspace bytes bpe_embed needs: 0, or, for a large output of a table of a
+ * wider type whose rows are read several times each, what sorting the IDs
+ * takes (always 0 for n_ids <= n_rows). */
+size_t bpe_embed_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t width, int weight_type,
+                                 int out_type);
+
 /*
  * out[t] = scale * weight[ids[t]], t in [0, n_ids).
  *  d_weight  [n_rows][width] of weight_type;  d_out  [n_ids][width] of out_type.
  *  pad_id    the ID that stands for no token (its rows of out are zeros), or -1.
  * An ID outside [0, n_rows) that is not pad_id gives a row of zeros and sets
- * BPE_STATUS_BAD_ID.  out must not overlap weight.
- * Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
+ * BPE_STATUS_BAD_ID.  out must not overlap weight.  d_workspace: device
+ * scratch, 16-byte aligned, of workspace_bytes >= bpe_embed_workspace_bytes of
+ * the same sizes and types (NULL where that is 0).
+ * Returns BPE_OK, BPE_EINVAL, BPE_EWORKSPACE or BPE_EHIP.
  */
 int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t width,
               int64_t weight_stride, const int32_t *d_ids, int64_t n_ids, float scale,
-              int32_t pad_id, void *d_out, int out_type, int64_t out_stride, int32_t *d_status,
-              void *hip_stream);
+              int32_t pad_id, void *d_out, int out_type, int64_t out_stride, void *d_workspace,
+              size_t workspace_bytes, int32_t *d_status, void *hip_stream);
 
 /* Workspace bytes bpe_embed_grad needs (0 for few IDs and for a size out of
  * range). */

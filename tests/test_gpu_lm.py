@@ -107,6 +107,31 @@ def test_embed_large(n, D, wt, ot):
     ref.check(got, want, ref.U * np.abs(want), "embed")
 
 
+@pytest.mark.parametrize("V,D,ot,extra", [(700, 1001, BF16, 3), (40, 4096, F16, 0), (9000, 2056, BF16, 0)])
+def test_embed_by_sorted_ids(V, D, ot, extra):
+    n = (512 << 20) // (2 * D) + 77
+    assert lm.embed_workspace_bytes(n, V, D, F32, ot) > 0
+    w = strided(randn((V, D), F32, 1), extra)
+    ids = ids_of(n, V, 2)
+    ids[::11] = V - 1
+    ids[5], ids[n - 1], ids[n // 2] = -1, V, -2**31
+    t, st = dev(ids), status()
+    got = lm.embed(w, t, 1.3, pad_id=V - 1, out_dtype=ot, status=st)
+    assert int(st.item()) == _lib.STATUS_BAD_ID
+    # the same bits as in pieces, which go by the IDs' own order
+    for a in range(0, n, 50000):
+        assert lm.embed_workspace_bytes(min(50000, n - a), V, D, F32, ot) == 0
+        assert torch.equal(got[a:a + 50000], lm.embed(w, t[a:a + 50000], 1.3, pad_id=V - 1, out_dtype=ot,
+                                                      status=st))
+    some = np.unique(np.concatenate([np.arange(70), np.arange(n - 70, n), [n // 2],
+                                     np.random.default_rng(3).integers(0, n, 500)]))
+    want = ref.embed(ref.f64(w), ids[some], float(np.float32(1.3)), V - 1)
+    ref.check(got[dev(some)], want, ref.U * np.abs(want))
+    # a workspace of the caller's
+    space = torch.empty(lm.embed_workspace_bytes(n, V, D, F32, ot), dtype=torch.uint8, device=device())
+    assert torch.equal(got, lm.embed(w, t, 1.3, pad_id=V - 1, out_dtype=ot, workspace=space, status=st))
+
+
 def test_embed_pad_outside_the_table():
     w = randn((10, 16), F32, 4)
     ids = np.array([3, 999, 9], np.int32)

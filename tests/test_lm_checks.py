@@ -43,8 +43,9 @@ def test_header_constants():
 
 
 def embed_rc(weight=P, wt=0, V=100, D=64, ws=64, ids=P, n=5, scale=1.0, pad=-1, out=P, ot=0, os_=64,
-             status=P):
-    return _lib.load().bpe_embed(weight, wt, V, D, ws, ids, n, scale, pad, out, ot, os_, status, None)
+             space=None, space_bytes=0, status=P):
+    return _lib.load().bpe_embed(weight, wt, V, D, ws, ids, n, scale, pad, out, ot, os_, space,
+                                 space_bytes, status, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -59,6 +60,18 @@ def test_embed_refuses(bad):
 
 def test_embed_of_nothing():
     assert embed_rc(n=0, weight=None, ids=None, out=None) == _lib.BPE_OK
+
+
+def test_embed_workspace():
+    assert lm.embed_workspace_bytes(64, 128256, 4096, torch.bfloat16, torch.bfloat16) == 0
+    assert lm.embed_workspace_bytes(0, 100, 64, torch.float32, torch.float32) == 0
+    assert lm.embed_workspace_bytes(1 << 20, 1 << 20, 4096, torch.float32, torch.bfloat16) == 0
+    big = dict(n=262144, V=32256, D=4096, ws=4096, os_=4096, ot=1)
+    need = lm.embed_workspace_bytes(262144, 32256, 4096, torch.float32, torch.bfloat16)
+    assert 16 * 262144 <= need <= 32 * 262144
+    assert embed_rc(**big, space=P, space_bytes=need - 1) == _lib.BPE_EWORKSPACE
+    assert embed_rc(**big, space=None, space_bytes=need) == _lib.BPE_EINVAL
+    assert embed_rc(**big, space=P + 8, space_bytes=need) == _lib.BPE_EINVAL
 
 
 def grad_rc(grad=P, gt=1, gs=64, ids=P, n=5000, V=100, D=64, scale=1.0, pad=-1, acc=0, out=P, ot=0,
