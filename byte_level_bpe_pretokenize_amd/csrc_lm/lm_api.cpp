@@ -27,7 +27,9 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width) {
   while ((n_rows >> bits) != 0) ++bits;
   L.passes = (bits + kDigitBits - 1) / kDigitBits;
   L.bits = (bits + L.passes - 1) / L.passes;
-  L.sort_tiles = (int32_t)((n_ids + kSortTile - 1) / kSortTile);
+  const int64_t steps = (n_ids + kSortTile - 1) / kSortTile;
+  L.sort_steps = (int32_t)((steps + kSortTiles - 1) / kSortTiles);
+  L.sort_tiles = L.sort_steps > 0 ? (int32_t)((steps + L.sort_steps - 1) / L.sort_steps) : 0;
   // long tiles for few cut rows, short ones where there would be too few waves
   const int64_t slabs = width < 8 ? 1 : (width + 511) / 512;
   L.tile = kGradTile;
@@ -77,6 +79,7 @@ void sort_args(GradArgs *a, const GradLayout &L, uint8_t *ws) {
   a->pos[1] = (int32_t *)(ws + L.pos1);
   a->counts = (int32_t *)(ws + L.counts);
   a->sort_tiles = L.sort_tiles;
+  a->sort_steps = L.sort_steps;
   a->passes = L.passes;
   a->bits = L.bits;
 }

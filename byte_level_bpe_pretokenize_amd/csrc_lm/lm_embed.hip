@@ -75,7 +75,7 @@ __device__ __forceinline__ int32_t grad_key(const GradArgs &a, int32_t id, bool 
 __global__ void __launch_bounds__(kSortThreads) k_grad_count(GradArgs a, int pass) {
   __shared__ int32_t cnt[kMaxDigits];
   const int tid = threadIdx.x, digits = 1 << a.bits;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortTile;
+  const int64_t i0 = (int64_t)blockIdx.x * kSortTile * a.sort_steps;
   for (int d = tid; d < digits; d += kSortThreads) cnt[d] = 0;
   if (pass == 0 && a.touched)
     for (int64_t v = (int64_t)blockIdx.x * kSortThreads + tid; v < a.n_rows;
@@ -83,12 +83,14 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_count(GradArgs a, int pas
       a.touched[v] = 0;
   __syncthreads();
   bool bad = false;
+  for (int s = 0; s < a.sort_steps; ++s) {
 #pragma unroll
-  for (int j = 0; j < kSortTile / kSortThreads; ++j) {
-    const int64_t i = i0 + j * kSortThreads + tid;
-    if (i < a.n_ids) {
-      const int32_t k = pass == 0 ? grad_key(a, a.ids[i], &bad) : a.key[(pass + 1) & 1][i];
-      atomicAdd(&cnt[(k >> (pass * a.bits)) & (digits - 1)], 1);
+    for (int j = 0; j < kSortTile / kSortThreads; ++j) {
+      const int64_t i = i0 + (int64_t)s * kSortTile + j * kSortThreads + tid;
+      if (i < a.n_ids) {
+        const int32_t k = pass == 0 ? grad_key(a, a.ids[i], &bad) : a.key[(pass + 1) & 1][i];
+        atomicAdd(&cnt[(k >> (pass * a.bits)) & (digits - 1)], 1);
+      }
     }
   }
   if (bad) atomicOr(a.status, (int32_t)BPE_STATUS_BAD_ID);
@@ -120,7 +122,8 @@ __device__ __forceinline__ bool place_key(int32_t key, int shift, int bits, int3
 // One pass's scatter of one tile.  A key's place: the keys of smaller digits
 // (the column sums of `counts`, scanned), the keys of its digit in earlier
 // tiles, in earlier waves of the tile and before it in its wave.  Each wave
-// takes 256 consecutive keys, 64 at a time.
+// takes sort_steps times 256 consecutive keys, 64 at a time; with more than one
+// step it reads them twice, to count and to place.
 __global__ void __launch_bounds__(kSortThreads) k_grad_scatter(GradArgs a, int pass) {
   constexpr int NW = kSortThreads / 64;
   constexpr int PER = kSortTile / kSortThreads;
@@ -129,24 +132,27 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_scatter(GradArgs a, int p
   const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
   const int digits = 1 << a.bits, shift = pass * a.bits;
   const bool last = pass == a.passes - 1;
-  const int64_t i0 = (int64_t)blockIdx.x * kSortTile + wv * (64 * PER);
+  const int64_t i0 = ((int64_t)blockIdx.x * kSortTile + wv * (64 * PER)) * a.sort_steps;
   for (int d = tid; d < NW * kMaxDigits; d += kSortThreads) (&base[0][0])[d] = 0;
   int32_t key[PER], pos[PER];
   bool bad = false;
+  auto load = [&](int s) {
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int64_t i = i0 + j * 64 + lane;
-    key[j] = -1;
-    pos[j] = (int32_t)i;
-    if (i < a.n_ids) {
-      if (pass == 0) {
-        key[j] = grad_key(a, a.ids[i], &bad);
-      } else {
-        key[j] = a.key[(pass + 1) & 1][i];
-        pos[j] = a.pos[(pass + 1) & 1][i];
+    for (int j = 0; j < PER; ++j) {
+      const int64_t i = i0 + s * (64 * PER) + j * 64 + lane;
+      key[j] = -1;
+      pos[j] = (int32_t)i;
+      if (i < a.n_ids) {
+        if (pass == 0) {
+          key[j] = grad_key(a, a.ids[i], &bad);
+        } else {
+          key[j] = a.key[(pass + 1) & 1][i];
+          pos[j] = a.pos[(pass + 1) & 1][i];
+        }
       }
     }
-  }
+  };
+  load(0);
   // thread d < digits: the digit's keys in all tiles and in the earlier ones
   int32_t all = 0, before = 0;
   if (tid < digits)
@@ -157,9 +163,13 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_scatter(GradArgs a, int p
       if (s < (int)blockIdx.x) before += c;
     }
   __syncthreads();
+  for (int s = 0;;) {
 #pragma unroll
-  for (int j = 0; j < PER; ++j)
-    if (key[j] >= 0) atomicAdd(&base[wv][(key[j] >> shift) & (digits - 1)], 1);
+    for (int j = 0; j < PER; ++j)
+      if (key[j] >= 0) atomicAdd(&base[wv][(key[j] >> shift) & (digits - 1)], 1);
+    if (++s == a.sort_steps) break;
+    load(s);
+  }
   int32_t total;
   const int32_t ex = block_excl_sum<int32_t, kSortThreads>(all, red, &total);
   if (tid < digits) {
@@ -171,13 +181,16 @@ __global__ void __launch_bounds__(kSortThreads) k_grad_scatter(GradArgs a, int p
     }
   }
   __syncthreads();
+  for (int s = 0; s < a.sort_steps; ++s) {
+    if (a.sort_steps > 1) load(s);
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    int32_t at;
-    if (!place_key(key[j], shift, a.bits, base[wv], &at)) continue;
-    a.key[pass & 1][at] = key[j];
-    a.pos[pass & 1][at] = pos[j];
-    if (last && a.touched && key[j] < a.n_rows) a.touched[key[j]] = 1;
+    for (int j = 0; j < PER; ++j) {
+      int32_t at;
+      if (!place_key(key[j], shift, a.bits, base[wv], &at)) continue;
+      a.key[pass & 1][at] = key[j];
+      a.pos[pass & 1][at] = pos[j];
+      if (last && a.touched && key[j] < a.n_rows) a.touched[key[j]] = 1;
+    }
   }
 }
 

@@ -35,7 +35,7 @@ struct EmbedArgs {
 
 // ---- the embedding's gradient ----------------------------------------------
 // The IDs are sorted (a stable radix sort of at most kDigitBits bits per pass,
-// tiles of kSortTile IDs); the sorted list is cut into tiles of `tile` IDs, one
+// in at most kSortTiles tiles, whose counts every workgroup reads); the sorted list is cut into tiles of `tile` IDs, one
 // wave per tile and 64 vectors of columns.
 constexpr int kEmbedUnits = 1024;  // vectors per workgroup of the forward
 constexpr int kZeroRows = 16;      // rows of the table per workgroup of zeros
@@ -48,6 +48,7 @@ constexpr int kDigitBits = 9;
 constexpr int kMaxDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 512;
 constexpr int kSortTile = 4 * kSortThreads;
+constexpr int kSortTiles = 256;
 
 struct GradArgs {
   const void *grad;
@@ -65,7 +66,8 @@ struct GradArgs {
   uint8_t *touched;          // [n_rows] 1: the ID occurs; or nullptr
   float *part;               // [tiles][2][width] sums of rows that a tile's edge cuts
   // launch
-  int32_t sort_tiles, passes, bits;  // bits of one pass's digit
+  int32_t sort_tiles, sort_steps;    // tiles of kSortTile * sort_steps IDs
+  int32_t passes, bits;              // bits of one pass's digit
   int32_t tile;                      // IDs per tile of the sums
   int32_t tiles;
   int32_t slabs;                     // column groups of 64 vectors
@@ -74,7 +76,7 @@ struct GradArgs {
 
 struct GradLayout {
   size_t key0, key1, pos0, pos1, counts, touched, part, total;
-  int32_t sort_tiles, passes, bits, tile, tiles;
+  int32_t sort_tiles, sort_steps, passes, bits, tile, tiles;
 };
 
 // a.key != nullptr: by sorted IDs, after the sort that `sort` describes.

@@ -240,7 +240,10 @@ class _Embedding(torch.autograd.Function):
         return embed(weight, ids, scale, pad_id=pad_id, out_dtype=out_dtype, status=status)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
+        if not ctx.needs_input_grad[0]:
+            return (None,) * 6
         (ids,) = ctx.saved_tensors
         n_rows, dtype, scale, pad_id, status = ctx.embed
         g = embed_grad(grad.contiguous(), ids, n_rows, scale, pad_id=pad_id, out_dtype=dtype,

@@ -193,6 +193,22 @@ def test_embed_grad_lengths(n, kind):
     assert torch.equal(got, lm.embed_grad(g, dev(ids), V))  # the same bits again
 
 
+@pytest.mark.parametrize("n,V,kind", [(524_289, 1000, "zipf"), (600_001, 300_000, "distinct"),
+                                      (1_700_003, 77, "zipf"), (1_100_000, 40, "one")])
+def test_embed_grad_many_ids(n, V, kind):
+    D = 16
+    g = randn((n, D), F32, n)
+    ids = ids_of(n, V, n, kind)
+    ids[::17] = V - 1
+    got = lm.embed_grad(g, dev(ids), V, pad_id=V - 1)
+    want, tol = ref.embed_grad(ref.f64(g), ids, V, 1.0, V - 1)
+    ref.check(got, want, tol, kind)
+    # whole numbers, so that every sum is exact: no position left out or twice
+    g = torch.randint(-8, 9, (n, D), device=device(), generator=gen(n)).float()
+    want, _ = ref.embed_grad(ref.f64(g), ids, V, 1.0, V - 1)
+    assert np.array_equal(ref.f64(lm.embed_grad(g, dev(ids), V, pad_id=V - 1)), want)
+
+
 @pytest.mark.parametrize("n", [100, 3001])
 @pytest.mark.parametrize("D", [5, 513, 2056])
 @pytest.mark.parametrize("ot", [F32, BF16])
