@@ -10,7 +10,8 @@ positions of a paged cache from the requests' lengths.
 Every call takes ``status``, an int32 device tensor of one element that the
 caller has cleared: the call ORs _lib.STATUS_* bits into it and does not
 synchronize.  Without one the call makes its own, waits for it, and raises
-where a bit is set.  Work goes to ``stream``, or the current stream.
+where a bit is set (so a call that is captured into a graph needs one).  Work
+goes to ``stream``, or the current stream.
 """
 from __future__ import annotations
 
@@ -156,7 +157,7 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
     dev = _device("embed", (weight, ids, out, workspace, status))
     L = _lib.load()
     st = _status(status, dev)
-    res = torch.empty((*ids.shape, D), dtype=dt, device=dev) if out is None else out
+    res = weight.new_empty((*ids.shape, D), dtype=dt) if out is None else out
     w_ptr, w_bytes = None, 0
     if workspace is not None:
         w_ptr, w_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -218,7 +219,7 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float 
     dev = _device("embed_grad", (grad, ids, out, workspace, status))
     L = _lib.load()
     st = _status(status, dev)
-    res = torch.empty((n_rows, D), dtype=dt, device=dev) if out is None else out
+    res = grad.new_empty((n_rows, D), dtype=dt) if out is None else out
     if workspace is None:
         w_bytes = L.bpe_embed_grad_workspace_bytes(n, n_rows, D)
         workspace = torch.empty(w_bytes, dtype=torch.uint8, device=dev) if w_bytes else None
@@ -336,7 +337,7 @@ def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = No
     dev = _device("process_logits", (logits, prompt_ids, prompt_off, out_ids, out_len, repetition,
                   frequency, presence, bias_off, bias_ids, bias_values, mask, mask_row, out, status))
     st = _status(status, dev)
-    res = torch.empty((B, V), dtype=dt, device=dev) if out is None else out
+    res = logits.new_empty((B, V), dtype=dt) if out is None else out
     a = _lib.LogitsArgs(logits.data_ptr(), ls, B, V, pp, n_prompt, po, mp, m_width, m_stride, ml,
                         rp, fp, sp, bi, bv, n_bias, bo, kp, k_rows, k_stride, kr, res.data_ptr(), os_, st.data_ptr(), lt, ot)
     rc = _lib.load().bpe_process_logits(C.byref(a), _stream(dev))
@@ -390,13 +391,13 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
     L = _lib.load()
     st = _status(status, dev)
     if slots is None:
-        slots = torch.empty(n_new, dtype=torch.int64, device=dev)
+        slots = new_off.new_empty(n_new)
     if positions is None:
-        positions = torch.empty(n_new, dtype=torch.int32, device=dev)
+        positions = cached.new_empty(n_new)
     if lengths is None:
-        lengths = torch.empty(R, dtype=torch.int32, device=dev)
+        lengths = cached.new_empty(R)
     if used is None:
-        used = torch.empty(1, dtype=torch.int64, device=dev)
+        used = new_off.new_empty(1)
     if workspace is None:
         w_bytes = L.bpe_block_tables_workspace_bytes(R, n_new)
         workspace = torch.empty(w_bytes, dtype=torch.uint8, device=dev) if w_bytes else None

@@ -313,6 +313,14 @@ def test_embedding_gradient_in_bfloat16():
     assert w.grad.dtype == BF16 and int(st.item()) == 0
 
 
+def test_embedding_has_no_second_derivative():
+    w = randn((30, 24), F32, 1).requires_grad_()
+    dy = randn((10, 24), F32, 2).requires_grad_()
+    (g,) = torch.autograd.grad(lm.embedding(w, dev(ids_of(10, 30, 3))), w, dy, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+
+
 # ---- logits -------------------------------------------------------------------------
 def logits_case(B, V, lt, seed, prompt=40, made=12, bias=5, masks=3, stride=0):
     rng = np.random.default_rng(seed)
