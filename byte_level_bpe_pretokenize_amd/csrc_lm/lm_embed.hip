@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(256) k_embed_runs(EmbedArgs a) {
         for (int e = 0; e < E; ++e)
           r.v[e] = from_f32<TO>(k != none ? (float)y[j].v[e] * a.scale : 0.f);
       }
-      if (mine)
-        store_vec<TO, E, true>((TO *)a.out + (int64_t)lane_value(pos, at + j) * a.o_stride + col, r);
+      const int64_t t = lane_value(pos, at + j);
+      if (mine) store_vec<TO, E, true>((TO *)a.out + t * a.o_stride + col, r);
     }
   };
   fetch(x[0], 0);
