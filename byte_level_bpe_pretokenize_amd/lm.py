@@ -12,6 +12,10 @@ caller has cleared: the call ORs _lib.STATUS_* bits into it and does not
 synchronize.  Without one the call makes its own, waits for it, and raises
 where a bit is set (so a call that is captured into a graph needs one).  Work
 goes to ``stream``, or the current stream.
+
+Only ``embedding`` takes part in autograd.  The other calls raise where grad
+mode is on and a matrix or vector given to them requires a gradient, which
+they would drop; what they write in place counts as modified.
 """
 from __future__ import annotations
 
@@ -30,6 +34,8 @@ _TYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _li
 _stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
     else lambda dev: torch.cuda.current_stream(dev).cuda_stream
 
+
+_modified = torch.autograd.graph.increment_version
 
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -109,6 +115,14 @@ def _end(name: str, rc: int, own: torch.Tensor | None) -> None:
             raise RuntimeError(f"{name} device status {st:#x}")
 
 
+def _no_gradient(name: str, instead: str, tensors) -> None:
+    """Refuses tensors whose gradient the call would drop."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError(f"{name} gives no gradient, and a tensor given to it requires one: "
+                               f"{instead}under torch.no_grad(), or with detached tensors")
+
+
 def _on(stream, call, tensors, *args, **kw):
     """The call with `stream` as the current stream: what it allocates belongs
     to that stream, and the tensors given to it are marked as used there, so
@@ -140,6 +154,7 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
     if stream is not None:
         return _on(stream, embed, (weight, ids, out, workspace, status), weight, ids, scale,
                    pad_id=pad_id, out=out, out_dtype=out_dtype, workspace=workspace, status=status)
+    _no_gradient("embed", "call embedding instead, or embed ", (weight, out))
     pad_id = _int32(pad_id, -1, "pad_id")
     wt = _type(weight.dtype, "weight")
     ws = _rows(weight, "weight")
@@ -168,6 +183,8 @@ def embed(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, pad_id
             w_ptr = workspace.data_ptr()
     rc = L.bpe_embed(weight.data_ptr(), wt, V, D, ws, ip, n, scale, pad_id, res.data_ptr(), ot,
                      os_, w_ptr, w_bytes, st.data_ptr(), _stream(dev))
+    if out is not None:
+        _modified(out)
     _end("bpe_embed", rc, st if status is None else None)
     return res
 
@@ -192,6 +209,7 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float 
         return _on(stream, embed_grad, (grad, ids, out, workspace, status), grad, ids, n_rows,
                    scale, pad_id=pad_id, out=out, out_dtype=out_dtype, accumulate=accumulate,
                    workspace=workspace, status=status)
+    _no_gradient("embed_grad", "call it ", (grad, out))
     pad_id = _int32(pad_id, -1, "pad_id")
     gt = _type(grad.dtype, "grad")
     ip = _list(ids, torch.int32, -1, "ids")
@@ -229,6 +247,8 @@ def embed_grad(grad: torch.Tensor, ids: torch.Tensor, n_rows: int, scale: float 
                           1 if accumulate else 0, res.data_ptr(), ot, os_,
                           None if workspace is None else workspace.data_ptr(), w_bytes,
                           st.data_ptr(), _stream(dev))
+    if out is not None:
+        _modified(out)
     _end("bpe_embed_grad", rc, st if status is None else None)
     return res
 
@@ -284,6 +304,8 @@ def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = No
                   bias_off=bias_off, bias_ids=bias_ids, bias_values=bias_values, mask=mask,
                   mask_row=mask_row, out=out, status=status)
         return _on(stream, process_logits, (logits, *kw.values()), logits, out_dtype=out_dtype, **kw)
+    _no_gradient("process_logits", "call it ",
+                 (logits, repetition, frequency, presence, bias_values, out))
     lt, ls = _type(logits.dtype, "logits"), _rows(logits, "logits")
     B, V = logits.shape
 
@@ -341,6 +363,8 @@ def process_logits(logits: torch.Tensor, *, prompt_ids: torch.Tensor | None = No
     a = _lib.LogitsArgs(logits.data_ptr(), ls, B, V, pp, n_prompt, po, mp, m_width, m_stride, ml,
                         rp, fp, sp, bi, bv, n_bias, bo, kp, k_rows, k_stride, kr, res.data_ptr(), os_, st.data_ptr(), lt, ot)
     rc = _lib.load().bpe_process_logits(C.byref(a), _stream(dev))
+    if out is not None:
+        _modified(out)
     _end("bpe_process_logits", rc, st if status is None else None)
     return res
 
@@ -390,6 +414,7 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
                   used, workspace, status))
     L = _lib.load()
     st = _status(status, dev)
+    given = [t for t in (table, slots, positions, lengths, used) if t is not None]
     if slots is None:
         slots = new_off.new_empty(n_new)
     if positions is None:
@@ -408,5 +433,6 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
                             lengths.data_ptr(), used.data_ptr(),
                             None if workspace is None else workspace.data_ptr(), w_bytes,
                             st.data_ptr(), _stream(dev))
+    _modified(given)
     _end("bpe_block_tables", rc, st if status is None else None)
     return slots, positions, lengths, used
