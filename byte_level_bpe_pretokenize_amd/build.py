@@ -17,7 +17,7 @@ SOURCES = [os.path.join(CSRC, f)
                      "bpe_api.cpp", "bpe_tables.cpp", "bpe_text.cpp")]
 # the operators on token IDs (include/bpe_lm.h)
 SOURCES += [os.path.join(PKG, "csrc_lm", f)
-            for f in ("lm_embed.hip", "lm_logits.hip", "lm_blocks.hip", "lm_api.cpp")]
+            for f in ("lm_embed.hip", "lm_logits.hip", "lm_blocks.hip", "lm_api.cpp", "lm_layout.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,5 +1,6 @@
-// lm_internal.h -- arguments and layouts shared by the host checks (lm_api.cpp)
-// and the kernels of the operators on token IDs.
+// lm_internal.h -- arguments and layouts shared by the host checks (lm_api.cpp),
+// the host's layouts (lm_layout.cpp) and the kernels of the operators on token
+// IDs.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -79,6 +80,8 @@ struct GradLayout {
   int32_t sort_tiles, sort_steps, passes, bits, tile, tiles;
 };
 
+bool by_sorted_ids(int64_t n_ids, int64_t n_rows, int64_t width, int wt, int ot);
+
 // a.key != nullptr: by sorted IDs, after the sort that `sort` describes.
 hipError_t launch_embed(const EmbedArgs &a, const GradArgs *sort, int wt, int ot,
                         hipStream_t stream);
@@ -116,6 +119,8 @@ constexpr int kBlockChunk = 2048;     // new tokens per workgroup
 constexpr int kBlockGroups = 256;     // groups of requests, at most
 constexpr int kBlockFused = 2048;     // requests that each workgroup sums by itself
 constexpr int kBlockScan = 1024;      // threads of the scan: requests per step
+
+void block_divisor(int32_t bs, uint32_t *magic, int32_t *shift);
 
 hipError_t launch_blocks(const BlockArgs &a, hipStream_t stream);
 

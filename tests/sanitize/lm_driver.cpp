@@ -1,0 +1,93 @@
+// What the host decides for the operators on token IDs (lm_layout.cpp), under
+// AddressSanitizer and UndefinedBehaviorSanitizer: workspace layouts and
+// divisors on the limits and on seeded random sizes.  One check by name per
+// run; built and run by tests/test_lm_layout.py.
+#include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include <algorithm>
+#include <random>
+#include <utility>
+#include <vector>
+
+#include "lm_internal.h"
+
+using namespace bpe;
+
+#define CHECK(c)                                                      \
+  do {                                                                \
+    if (!(c)) {                                                       \
+      fprintf(stderr, "check failed: %s (line %d)\n", #c, __LINE__); \
+      exit(3);                                                        \
+    }                                                                 \
+  } while (0)
+
+static std::mt19937_64 rng(20261206);
+
+// Between lo and hi, spread over the logarithm.
+static int64_t between(int64_t lo, int64_t hi) {
+  const double x = std::uniform_real_distribution<double>(0, 1)(rng);
+  const double v = (double)lo * __builtin_pow((double)hi / (double)lo, x);
+  return std::min(hi, std::max(lo, (int64_t)v));
+}
+
+// Regions in order, aligned, each as large as what goes into it; digits that
+// hold every value; tiles that hold every ID.
+static void check_layout(int64_t n, int64_t V, int64_t D) {
+  const GradLayout L = grad_layout(n, V, D);
+  CHECK(L.bits >= 1 && L.bits <= kDigitBits && L.passes * L.bits < 32);
+  CHECK(V >> (L.passes * L.bits) == 0);
+  CHECK(L.sort_tiles >= 1 && L.sort_tiles <= kSortTiles);
+  const int64_t per = (int64_t)kSortTile * L.sort_steps;
+  CHECK(L.sort_tiles * per >= n && (L.sort_tiles - 1) * per < n);
+  CHECK(L.tile >= 8 && L.tile <= kGradTile);
+  CHECK((int64_t)L.tiles * L.tile >= n && (int64_t)(L.tiles - 1) * L.tile < n);
+  const std::vector<std::pair<size_t, size_t>> regions = {
+      {L.key0, (size_t)n * 4}, {L.key1, (size_t)n * 4}, {L.pos0, (size_t)n * 4},
+      {L.pos1, (size_t)n * 4}, {L.counts, ((size_t)L.sort_tiles << L.bits) * 4},
+      {L.touched, ((size_t)V + 15) / 16 * 16},  // cleared in whole 16-byte groups
+      {L.part, (size_t)L.tiles * 2 * (size_t)D * 4}};
+  size_t end = 0;
+  for (const auto &r : regions) {
+    CHECK(r.first % 256 == 0 && r.first >= end);
+    end = r.first + r.second;
+  }
+  CHECK(L.total >= end);
+}
+
+static void layout() {
+  for (int64_t n : {(int64_t)1, (int64_t)kGradDirect + 1, (int64_t)kGradSmall, (int64_t)BPE_MAX_IDS})
+    for (int64_t V : {(int64_t)1, (int64_t)511, (int64_t)512, (int64_t)BPE_MAX_ROWS})
+      for (int64_t D : {1, 7, 8, 513, BPE_MAX_WIDTH}) check_layout(n, V, D);
+  for (int i = 0; i < 20000; ++i)
+    check_layout(between(1, BPE_MAX_IDS), between(1, BPE_MAX_ROWS), between(1, BPE_MAX_WIDTH));
+}
+
+static void divisor() {
+  for (int i = 0; i < 3000; ++i) {
+    const int32_t bs = i < 300 ? i + 2 : (int32_t)between(2, INT32_MAX);
+    uint32_t magic;
+    int32_t shift;
+    block_divisor(bs, &magic, &shift);
+    CHECK(shift >= 0 && shift < 31);
+    for (int j = 0; j < 300; ++j) {
+      const int64_t q = between(1, (int64_t)INT32_MAX / bs + 1);
+      for (int64_t x : {q * bs - 1, q * bs, (int64_t)(rng() >> 33), (int64_t)INT32_MAX - j, (int64_t)j})
+        if (x <= INT32_MAX)
+          CHECK((int64_t)(((uint64_t)x * magic >> 32) >> shift) == x / bs);
+    }
+  }
+}
+
+int main(int argc, char **argv) {
+  const std::pair<const char *, void (*)()> checks[] = {{"layout", layout}, {"divisor", divisor}};
+  for (const auto &c : checks)
+    if (argc == 2 && !strcmp(argv[1], c.first)) {
+      c.second();
+      printf("passed\n");
+      return 0;
+    }
+  fprintf(stderr, "no such check\n");
+  return 2;
+}
