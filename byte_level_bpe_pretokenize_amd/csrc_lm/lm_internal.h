@@ -92,6 +92,8 @@ hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);
 // ---- logits ------------------------------------------------------------------
 constexpr int kLogitSlab = 4096;  // logits per workgroup, at least
 
+bool logits_wide(const bpe_logits_args &a);
+
 hipError_t launch_logits(const bpe_logits_args &a, hipStream_t stream);
 
 // ---- block tables --------------------------------------------------------------

@@ -288,21 +288,17 @@ hipError_t logits_launch(const bpe_logits_args &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Long lists are read by wide workgroups, in half as many slabs (24 rows of
-// 100,256 logits with 26,000 prompt IDs each: 18 us with 1024 threads, 26 with
-// 256); short ones leave narrow workgroups ahead (256 rows of 128,256 with 600:
-// 75 and 39 us).
 template <typename TI, typename TO, bool STREAM>
-hipError_t logits_wide(const bpe_logits_args &a, hipStream_t stream) {
-  const bool longer = a.n_prompt / a.rows + a.made_width > 4096;
-  return longer ? logits_launch<TI, TO, 1024, 2 * kLogitSlab, STREAM>(a, stream)
-                : logits_launch<TI, TO, 256, kLogitSlab, STREAM>(a, stream);
+hipError_t logits_wide_or_not(const bpe_logits_args &a, hipStream_t stream) {
+  return logits_wide(a) ? logits_launch<TI, TO, 1024, 2 * kLogitSlab, STREAM>(a, stream)
+                        : logits_launch<TI, TO, 256, kLogitSlab, STREAM>(a, stream);
 }
 
 template <typename TI, typename TO>
 hipError_t logits_as(const bpe_logits_args &a, hipStream_t stream) {
   const bool big = a.rows * a.vocab * (int64_t)sizeof(TO) >= kStreamBytes;
-  return big ? logits_wide<TI, TO, true>(a, stream) : logits_wide<TI, TO, false>(a, stream);
+  return big ? logits_wide_or_not<TI, TO, true>(a, stream)
+             : logits_wide_or_not<TI, TO, false>(a, stream);
 }
 
 template <typename TI>

@@ -80,8 +80,27 @@ static void divisor() {
   }
 }
 
+// The logits' variant goes by the lists' lengths, not by the room for them.
+static void variant() {
+  bpe_logits_args a = {};
+  for (int64_t rows : {1, 24, 256})
+    for (int64_t prompt : {0, 600, 4096, 5000, 75000}) {
+      a.rows = rows;
+      a.vocab = 128256;
+      a.n_prompt = rows * prompt;
+      a.made_width = 0;
+      const bool wide = logits_wide(a);
+      CHECK(wide == (prompt > 4096));
+      for (int64_t width : {1, 256, 4096, 8192, 1 << 20}) {
+        a.made_width = width;
+        CHECK(logits_wide(a) == wide);
+      }
+    }
+}
+
 int main(int argc, char **argv) {
-  const std::pair<const char *, void (*)()> checks[] = {{"layout", layout}, {"divisor", divisor}};
+  const std::pair<const char *, void (*)()> checks[] = {{"layout", layout}, {"divisor", divisor},
+                                                         {"variant", variant}};
   for (const auto &c : checks)
     if (argc == 2 && !strcmp(argv[1], c.first)) {
       c.second();
