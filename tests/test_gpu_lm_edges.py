@@ -1,13 +1,16 @@
 """The operators on token IDs on the GPU at the edges of their kernels' variants:
-column slabs with few lanes in use, queues that overflow, the launches of the
-largest batches.  Bounds as in test_gpu_lm.py."""
+column slabs with few lanes in use, queues that overflow, wide workgroups, batches
+past the caches, inputs that die under a call.  Bounds as in test_gpu_lm.py."""
+import numpy as np
 import pytest
 import torch
 
+import lm_reference as ref
 from byte_level_bpe_pretokenize_amd import lm
 
 from gpu_util import device
-from test_gpu_lm import BF16, F32, gaps, gen, randn, status, strided
+from test_gpu_lm import (BF16, F16, F32, blocks_case, check_blocks, dev, gaps, gen, ids_of, randn,
+                         status, strided)
 
 pytestmark = pytest.mark.gpu
 
@@ -31,3 +34,155 @@ def test_embed_by_sorted_ids_few_lanes(D):
         want = (w * 0.5).to(ot)[ids[a:a + step].long()]
         assert torch.equal(out[a:a + step], want), (D, a)
     assert torch.all(gaps(out, 3) == 0)
+
+
+# ---- the gradient by sorted IDs, float32 to half precision ------------------------
+@pytest.mark.parametrize("ot", [BF16, F16])
+@pytest.mark.parametrize("n,V,D", [(2049, 90, 7), (3001, 1500, 72), (6144, 300, 513), (6145, 300, 520),
+                                   (40000, 2000, 1001)])
+def test_embed_grad_narrows(n, V, D, ot):
+    g = randn((n, D), F32, n)
+    ids = ids_of(n, V, n)
+    ids[5], ids[n - 1] = -1, V
+    st = status()
+    got = lm.embed_grad(g, dev(ids), V, 0.3, out_dtype=ot, status=st)
+    want, tol = ref.embed_grad(ref.f64(g), ids, V, float(np.float32(0.3)))
+    ref.check(got, want, tol, "embed_grad")
+    first = randn((V, D), ot, 9)
+    out = first.clone()
+    lm.embed_grad(g, dev(ids), V, 0.3, out=out, accumulate=True, status=st)
+    base = ref.f64(first)
+    ref.check(out, base + want, tol + ref.U * (np.abs(base) + np.abs(want)), "accumulate")
+
+
+@pytest.mark.parametrize("n", [2049, 5000, 9000])
+def test_embedding_of_a_bfloat16_table_to_float32(n):
+    w = randn((70, 264), BF16, 1).requires_grad_()
+    ids = ids_of(n, 70, 2)
+    dy = randn((n, 264), F32, 3)
+    st = status()
+    lm.embedding(w, dev(ids), 2.0, out_dtype=F32, status=st).backward(dy)
+    want, tol = ref.embed_grad(ref.f64(dy), ids, 70, 2.0)
+    assert w.grad.dtype == BF16 and int(st.item()) == 0
+    ref.check(w.grad, want, tol)
+
+
+# ---- logits: queues that overflow, wide workgroups with a queue ----------------------
+def check_logits(V, lists, lt, ot, seed):
+    """lists: for each row its prompt, its generated IDs and how many biases."""
+    rng = np.random.default_rng(seed)
+    B = len(lists)
+    x = randn((B, V), lt, seed).mul_(3)
+    prompts, made = [np.asarray(r[0]) for r in lists], [np.asarray(r[1]) for r in lists]
+    out_ids = np.zeros((B, max(len(m) for m in made)), np.int32)
+    for b, m in enumerate(made):
+        out_ids[b, :len(m)] = m
+    biases = [{int(v): float(np.float32(rng.uniform(-5, 5)))
+               for v in np.sort(rng.choice(V, r[2], replace=False))} for r in lists]
+    par = {k: rng.uniform(lo, hi, B).astype(np.float32)
+           for k, lo, hi in (("repetition", 0.7, 1.6), ("frequency", -0.5, 1.0), ("presence", -0.5, 1.0))}
+    mask = rng.integers(0, 2**32, (2, (V + 31) // 32), dtype=np.uint64).astype(np.uint32)
+    row = np.arange(B, dtype=np.int32) % 3 - 1
+    cat = lambda a, t: dev(np.concatenate(a).astype(t))  # noqa: E731
+    off = lambda a: dev(np.concatenate([[0], np.cumsum([len(p) for p in a])]).astype(np.int64))  # noqa: E731
+    st = status()
+    got = lm.process_logits(
+        x, prompt_ids=cat(prompts, np.int32), prompt_off=off(prompts), out_ids=dev(out_ids),
+        out_len=dev(np.array([len(m) for m in made], np.int32)), bias_off=off(biases),
+        bias_ids=cat([np.array(list(b), np.int64) for b in biases], np.int32),
+        bias_values=cat([np.array(list(b.values())) for b in biases], np.float32),
+        mask=dev(mask.view(np.int32)), mask_row=dev(row), out_dtype=ot, status=st,
+        **{k: dev(v) for k, v in par.items()})
+    want, tol = ref.process_logits(ref.f64(x), [p.tolist() for p in prompts], [m.tolist() for m in made],
+                                   par["repetition"], par["frequency"], par["presence"], biases, mask, row)
+    ref.check(got, want, tol, "logits")
+    assert int(st.item()) == 0
+
+
+def distinct(lo, hi, n, seed):
+    return np.random.default_rng(seed).permutation(np.arange(lo, hi))[:n]
+
+
+@pytest.mark.parametrize("lt,ot", [(F32, F32), (BF16, F32), (F16, F16)])
+def test_logits_queue_overflows(lt, ot):
+    """256 threads: lists that fit one step, with more distinct tokens in a slab
+    than its queue has places (512); exactly 512; one more."""
+    V = 9000
+    check_logits(V, [(distinct(0, 4096, 1000, 1), distinct(0, 4096, 1000, 2), 200),
+                     (distinct(4096, 8192, 1024, 3), [], 0),
+                     (distinct(0, 4096, 512, 4), [], 0),
+                     (distinct(0, 4096, 513, 5), distinct(8192, V, 600, 6), 256),
+                     ([], distinct(4000, 4700, 700, 7), 3)], lt, ot, 8)
+
+
+@pytest.mark.parametrize("lt,ot", [(F32, F32), (BF16, F32), (BF16, BF16)])
+def test_logits_wide_workgroups(lt, ot):
+    """1,024 threads, which the batch's average prompt chooses, on rows of every
+    kind: short lists (a queue), more distinct tokens in a slab than its queue
+    has places (1,024), up to 1,024 biases with a queue and more without."""
+    V = 17000
+    rng = np.random.default_rng(1)
+    check_logits(V, [(rng.integers(0, V, 60000), [], 0),
+                     (rng.integers(0, V, 5), rng.integers(0, V, 9), 4),
+                     ([], [], 0),
+                     (distinct(0, 8192, 3000, 2), distinct(0, 8192, 3000, 3), 10),
+                     (distinct(0, 8192, 1024, 4), [], 0),
+                     (distinct(8192, 16384, 1025, 5), distinct(16384, V, 600, 6), 5),
+                     (rng.integers(0, V, 40), rng.integers(0, V, 50), 513),
+                     (rng.integers(0, V, 40), [], 600),
+                     ([], rng.integers(0, V, 4096), 1000),
+                     (rng.integers(0, V, 4096), [], 1024),
+                     (rng.integers(0, V, 7), [3, 3, 3], 1025),
+                     (rng.integers(0, V, 4097), rng.integers(0, V, 4100), 700)], lt, ot, 9)
+
+
+@pytest.mark.parametrize("lt,ot", [(F32, F32), (BF16, F32), (F32, BF16)])
+def test_logits_wide_workgroups_past_the_caches(lt, ot):
+    V = 2_000_003
+    rng = np.random.default_rng(2)
+    check_logits(V, [(rng.integers(0, V, 50000), rng.integers(0, V, 700), 30)] +
+                 [(rng.integers(0, V, 20), rng.integers(0, V, 5000), 600)] * 8, lt, ot, 10)
+
+
+# ---- block tables past the caches ----------------------------------------------------
+@pytest.mark.parametrize("R,most,bs", [(2048, 4000, 48), (30, 300_000, 16), (5000, 1600, 16), (2049, 4000, 1)])
+def test_blocks_past_the_caches(R, most, bs):
+    off, c, free, table = blocks_case(R, bs, R, most=most, cached=500)
+    assert off[-1] * 12 >= 32 << 20
+    assert check_blocks(off, c, free, table, bs) == 0
+
+
+# ---- another stream -------------------------------------------------------------------
+def test_another_stream_outlives_its_inputs():
+    """The inputs' last references go right after the calls, while these still
+    wait for earlier work of their stream; what is allocated then is not what
+    they read."""
+    V, D, n = 900, 136, 5000
+    make = lambda k: (randn((V, D), F32, k), dev(ids_of(n, V, k)), randn((n, D), BF16, k),  # noqa: E731
+                      randn((8, 5000), F32, k), dev(ids_of(8 * 64, 5000, k).reshape(8, 64)),
+                      torch.full((8,), 64, dtype=torch.int32, device=device()),
+                      torch.full((8,), 0.5, device=device()))
+
+    def calls(t, st, stream=None):
+        return (lm.embed(t[0], t[1], 2.0, status=st, stream=stream),
+                lm.embed_grad(t[2], t[1], V, status=st, stream=stream),
+                lm.process_logits(t[3], out_ids=t[4], out_len=t[5], frequency=t[6], status=st, stream=stream))
+
+    want = calls(make(1), status())
+    busy = torch.ones((4096, 4096), device=device())
+    side, st = torch.cuda.Stream(), status()
+    for _ in range(3):
+        inputs = make(1)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                busy = busy @ busy * 2.0 ** -12
+        got = calls(inputs, st, side)
+        del inputs
+        noise = [make(2) for _ in range(2)]
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        del noise
+    assert int(st.item()) == 0
