@@ -136,7 +136,7 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
 int bpe_process_logits(const bpe_logits_args *args, void *hip_stream) {
   if (!args) return BPE_EINVAL;
   const bpe_logits_args &a = *args;
-  if (!type_ok(a.logits_type) || !type_ok(a.out_type) || a.rows < 0 || a.rows > kMaxGrid ||
+  if (!type_ok(a.logits_type) || !type_ok(a.out_type) || a.rows < 0 || a.rows > BPE_MAX_IDS ||
       a.vocab < 0 || a.vocab > BPE_MAX_ROWS || !stride_ok(a.logits_stride, a.vocab) ||
       !stride_ok(a.out_stride, a.vocab) || !a.status)
     return BPE_EINVAL;
@@ -161,7 +161,7 @@ int bpe_process_logits(const bpe_logits_args *args, void *hip_stream) {
     return BPE_EINVAL;
   if (a.mask && !stride_ok(a.mask_stride, (a.vocab + 31) / 32)) return BPE_EINVAL;
   if (!any) return BPE_OK;
-  if ((a.vocab / kLogitSlab + 1) * a.rows > kMaxGrid) return BPE_EINVAL;
+  if (!logits_fit(a)) return BPE_EINVAL;
   return launch_logits(a, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }
 

@@ -14,6 +14,11 @@ namespace bpe {
 // up to 512 a workgroup).
 constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
 
+// Whether that many workgroups of so many threads are one launch.
+inline bool launch_fits(int64_t groups, int threads) {
+  return groups <= (((int64_t)1 << 32) - 1) / threads;
+}
+
 // Outputs of at least this size are stored past the caches (they are larger
 // than the L2s together, so nothing of them is there when they are read).
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
@@ -90,8 +95,13 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width);
 hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);
 
 // ---- logits ------------------------------------------------------------------
-constexpr int kLogitSlab = 4096;  // logits per workgroup, at least
+constexpr int kLogitSlab = 4096;         // logits per workgroup,
+constexpr int kLogitThreads = 256;       // and threads;
+constexpr int kLogitWideSlab = 8192;     // the same of the wide ones
+constexpr int kLogitWideThreads = 1024;
 
+// (rows > 0)
+bool logits_fit(const bpe_logits_args &a);
 bool logits_wide(const bpe_logits_args &a);
 
 hipError_t launch_logits(const bpe_logits_args &a, hipStream_t stream);

@@ -55,6 +55,11 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width) {
   return L;
 }
 
+// Whether the logits are one launch.
+bool logits_fit(const bpe_logits_args &a) {
+  return launch_fits((a.vocab + kLogitSlab - 1) / kLogitSlab * a.rows, kLogitThreads);
+}
+
 // Whether logits go by workgroups of 1,024 threads and slabs of 8,192 instead of
 // 256 and 4,096: where prompts are long on average, since those read a list in
 // fewer steps and half as many slabs.  Lists of 30,000 IDs: 24 rows of 100,256
@@ -63,7 +68,12 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width) {
 // do not count: the host has the width of their matrix, which a server makes as
 // wide as a generation may ever get, and not how many there are (256 rows with
 // room for 8,192 and 128 there: 42 and 35 us; all 8,192 there: 66 and 59).
-bool logits_wide(const bpe_logits_args &a) { return a.n_prompt / a.rows > 4096; }
+// Where the wide launch would have too many threads (2^22 rows and more) the
+// narrow one, which has fewer, is taken.
+bool logits_wide(const bpe_logits_args &a) {
+  const int64_t slabs = (a.vocab + kLogitWideSlab - 1) / kLogitWideSlab;
+  return a.n_prompt / a.rows > 4096 && launch_fits(slabs * a.rows, kLogitWideThreads);
+}
 
 // x / bs = x * magic >> (31 + s) with 2^s >= bs and magic = 2^(31 + s) / bs + 1:
 // magic * bs - 2^(31 + s) <= bs, so for x < 2^31 the error stays below 1 / bs.

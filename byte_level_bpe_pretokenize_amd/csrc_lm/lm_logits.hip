@@ -290,8 +290,8 @@ hipError_t logits_launch(const bpe_logits_args &a, hipStream_t stream) {
 
 template <typename TI, typename TO, bool STREAM>
 hipError_t logits_wide_or_not(const bpe_logits_args &a, hipStream_t stream) {
-  return logits_wide(a) ? logits_launch<TI, TO, 1024, 2 * kLogitSlab, STREAM>(a, stream)
-                        : logits_launch<TI, TO, 256, kLogitSlab, STREAM>(a, stream);
+  return logits_wide(a) ? logits_launch<TI, TO, kLogitWideThreads, kLogitWideSlab, STREAM>(a, stream)
+                        : logits_launch<TI, TO, kLogitThreads, kLogitSlab, STREAM>(a, stream);
 }
 
 template <typename TI, typename TO>

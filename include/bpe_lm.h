@@ -128,7 +128,7 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
  *              lets v through; -1: no mask.  Another row number outside
  *              [0, n_masks) sets BPE_STATUS_BAD_MASK_ROW and masks nothing.
  * IDs outside [0, vocab) in any list set BPE_STATUS_BAD_ID and count for
- * nothing.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
+ * nothing.  rows * ceil(vocab / 4096) < 2^24.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */
 typedef struct {
   const void *logits;

@@ -98,9 +98,39 @@ static void variant() {
     }
 }
 
+// The launch of the logits that pass the checks has fewer than 2^32 threads,
+// also where the lists choose wide workgroups, and the header's bound is the
+// one that is checked.
+static void logits_limit() {
+  bpe_logits_args a = {};
+  int fits = 0, wide = 0;
+  for (int i = 0; i < 200000; ++i) {
+    a.vocab = i % 2 ? between(1, 9000) : between(1, BPE_MAX_ROWS);
+    const int64_t slabs = (a.vocab + 4095) / 4096;
+    a.rows = i % 3 ? between(1, BPE_MAX_IDS) : ((int64_t)1 << 24) / slabs + (int64_t)(rng() % 5) - 2;
+    if (a.rows < 1) continue;
+    a.n_prompt = a.rows * between(1, 100000);
+    a.made_width = between(1, 1 << 20);
+    CHECK(logits_fit(a) == (a.rows * slabs < (int64_t)1 << 24));
+    if (!logits_fit(a)) continue;
+    ++fits;
+    wide += logits_wide(a);
+    const int64_t per = logits_wide(a) ? 8192 : 4096, threads = logits_wide(a) ? 1024 : 256;
+    CHECK((a.vocab + per - 1) / per * a.rows * threads < (int64_t)1 << 32);
+  }
+  CHECK(fits > 1000 && wide > 1000);
+  a.rows = (int64_t)1 << 22;
+  a.vocab = 100;
+  a.n_prompt = a.rows * 5000;
+  CHECK(logits_fit(a) && !logits_wide(a));
+  --a.rows;
+  CHECK(logits_wide(a));
+}
+
 int main(int argc, char **argv) {
   const std::pair<const char *, void (*)()> checks[] = {{"layout", layout}, {"divisor", divisor},
-                                                         {"variant", variant}};
+                                                         {"variant", variant},
+                                                         {"logits_limit", logits_limit}};
   for (const auto &c : checks)
     if (argc == 2 && !strcmp(argv[1], c.first)) {
       c.second();

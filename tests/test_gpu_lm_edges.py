@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import lm_reference as ref
-from byte_level_bpe_pretokenize_amd import lm
+from byte_level_bpe_pretokenize_amd import BPEError, lm
 
 from gpu_util import device
 from test_gpu_lm import (BF16, F16, F32, blocks_case, check_blocks, dev, gaps, gen, ids_of, randn,
@@ -142,6 +142,22 @@ def test_logits_wide_workgroups_past_the_caches(lt, ot):
     rng = np.random.default_rng(2)
     check_logits(V, [(rng.integers(0, V, 50000), rng.integers(0, V, 700), 30)] +
                  [(rng.integers(0, V, 20), rng.integers(0, V, 5000), 600)] * 8, lt, ot, 10)
+
+
+@pytest.mark.parametrize("B", [(1 << 23) + 5, (1 << 24) - 1])
+def test_logits_of_very_many_rows(B):
+    """Up to the launch with the most workgroups: 2^24 - 1."""
+    V = 3
+    x = torch.randn((B, V), device=device(), generator=gen(1))
+    made = torch.randint(0, V, (B, 1), dtype=torch.int32, device=device(), generator=gen(2))
+    st = status()
+    got = lm.process_logits(x, out_ids=made, out_len=torch.ones(B, dtype=torch.int32, device=device()),
+                            presence=torch.full((B,), 0.5, device=device()), status=st)
+    want = x - 0.5 * (torch.arange(V, device=device()) == made)
+    assert torch.equal(got, want) and int(st.item()) == 0
+    more = torch.zeros(((1 << 24), V), device=device())
+    with pytest.raises(BPEError):
+        lm.process_logits(more)
 
 
 # ---- block tables past the caches ----------------------------------------------------

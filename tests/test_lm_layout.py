@@ -26,7 +26,7 @@ def driver(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("check", ["layout", "divisor", "variant"])
+@pytest.mark.parametrize("check", ["layout", "divisor", "variant", "logits_limit"])
 def test_layout(driver, check):
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=1:verify_asan_link_order=0",
                UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
