@@ -87,7 +87,9 @@ int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t wid
 }
 
 size_t bpe_embed_grad_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t width) {
-  if (n_ids <= kGradDirect || n_ids > BPE_MAX_IDS || !table_ok(n_rows, width)) return 0;
+  if (n_ids <= kGradDirect || n_ids > BPE_MAX_IDS || !table_ok(n_rows, width) ||
+      !grad_fits(n_ids, n_rows, width))
+    return 0;
   return grad_layout(n_ids, n_rows, width).total;
 }
 
@@ -115,6 +117,7 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
   a.scale = scale;
   a.accumulate = accumulate != 0;
   if (n_ids > kGradDirect) {
+    if (!grad_fits(n_ids, n_rows, width)) return BPE_EINVAL;
     const GradLayout L = grad_layout(n_ids, n_rows, width);
     if (workspace_bytes < L.total) return BPE_EWORKSPACE;
     if ((uintptr_t)d_workspace & 15) return BPE_EINVAL;
@@ -124,9 +127,6 @@ int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const
     a.part = (float *)(ws + L.part);
     a.tile = L.tile;
     a.tiles = L.tiles;
-    // one workgroup per tile and slab of 64 vectors, and one per kZeroRows rows
-    const int64_t slabs = width < 8 ? 1 : (width + 511) / 512;
-    if (L.tiles * slabs > kMaxGrid - BPE_MAX_ROWS / kZeroRows) return BPE_EINVAL;
   }
   return launch_embed_grad(a, grad_type, out_type, (hipStream_t)hip_stream) == hipSuccess
              ? BPE_OK

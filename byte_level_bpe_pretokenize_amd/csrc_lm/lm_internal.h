@@ -92,6 +92,7 @@ hipError_t launch_embed(const EmbedArgs &a, const GradArgs *sort, int wt, int ot
                         hipStream_t stream);
 
 GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width);
+bool grad_fits(int64_t n_ids, int64_t n_rows, int64_t width);
 hipError_t launch_embed_grad(GradArgs a, int gt, int ot, hipStream_t stream);
 
 // ---- logits ------------------------------------------------------------------

@@ -55,6 +55,16 @@ GradLayout grad_layout(int64_t n_ids, int64_t n_rows, int64_t width) {
   return L;
 }
 
+// Whether the sums of a sorted gradient (four tiles and slabs of 512 columns, or
+// 16 rows of zeros, per workgroup) and the join of what tile edges cut (one
+// tile and slab) are one launch each.
+bool grad_fits(int64_t n_ids, int64_t n_rows, int64_t width) {
+  const int64_t slabs = width < 8 ? 1 : (width + 511) / 512;
+  const int64_t tiles = grad_layout(n_ids, n_rows, width).tiles * slabs;
+  return launch_fits((tiles + 3) / 4 + (n_rows + kZeroRows - 1) / kZeroRows, 256) &&
+         launch_fits(tiles, 256);
+}
+
 // Whether the logits are one launch.
 bool logits_fit(const bpe_logits_args &a) {
   return launch_fits((a.vocab + kLogitSlab - 1) / kLogitSlab * a.rows, kLogitThreads);

@@ -76,7 +76,7 @@ int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t wid
               int32_t pad_id, void *d_out, int out_type, int64_t out_stride, void *d_workspace,
               size_t workspace_bytes, int32_t *d_status, void *hip_stream);
 
-/* Workspace bytes bpe_embed_grad needs (0 for few IDs and for a size out of
+/* Workspace bytes bpe_embed_grad needs (0 for few IDs and for sizes out of
  * range). */
 size_t bpe_embed_grad_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t width);
 
@@ -91,7 +91,7 @@ size_t bpe_embed_grad_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t wid
  * which set BPE_STATUS_BAD_ID.  Each row's terms are added in float32 in an
  * order that the IDs alone fix.  d_workspace: device scratch, 16-byte aligned,
  * of workspace_bytes >= bpe_embed_grad_workspace_bytes(n_ids, n_rows, width)
- * (NULL where that is 0).
+ * (NULL where that is 0).  ceil(n_ids / 256) * ceil(width / 512) < 2^24.
  * Returns BPE_OK, BPE_EINVAL, BPE_EWORKSPACE or BPE_EHIP.
  */
 int bpe_embed_grad(const void *d_grad, int grad_type, int64_t grad_stride, const int32_t *d_ids,

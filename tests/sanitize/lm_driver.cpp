@@ -98,6 +98,30 @@ static void variant() {
     }
 }
 
+// A gradient that passes the checks has launches of fewer than 2^32 threads,
+// and the header's bound is the one that is checked.
+static void grad_limit() {
+  int fits = 0, not_ = 0;
+  for (int i = 0; i < 100000; ++i) {
+    const int64_t n = between(kGradDirect + 1, BPE_MAX_IDS), V = between(1, BPE_MAX_ROWS);
+    int64_t D = between(1, BPE_MAX_WIDTH);
+    if (i % 2) D = std::min<int64_t>(BPE_MAX_WIDTH, ((int64_t)1 << 32) / n * 512 + (int64_t)(rng() % 1025) + 1);
+    const GradLayout L = grad_layout(n, V, D);
+    const int64_t slabs = (D + 511) / 512;
+    CHECK(grad_fits(n, V, D) == ((n + 255) / 256 * slabs < (int64_t)1 << 24));
+    if (!grad_fits(n, V, D)) {
+      ++not_;
+      continue;
+    }
+    ++fits;
+    CHECK(((L.tiles * slabs + 3) / 4 + (V + kZeroRows - 1) / kZeroRows) * 256 < (int64_t)1 << 32);
+    CHECK(L.tiles * slabs * 256 < (int64_t)1 << 32);
+  }
+  CHECK(fits > 1000 && not_ > 1000);
+  CHECK(grad_fits(BPE_MAX_IDS, BPE_MAX_ROWS, 8) && grad_fits(BPE_MAX_IDS, 1, 1536));
+  CHECK(!grad_fits(BPE_MAX_IDS, 1, 1537));
+}
+
 // The launch of the logits that pass the checks has fewer than 2^32 threads,
 // also where the lists choose wide workgroups, and the header's bound is the
 // one that is checked.
@@ -130,6 +154,7 @@ static void logits_limit() {
 int main(int argc, char **argv) {
   const std::pair<const char *, void (*)()> checks[] = {{"layout", layout}, {"divisor", divisor},
                                                          {"variant", variant},
+                                                         {"grad_limit", grad_limit},
                                                          {"logits_limit", logits_limit}};
   for (const auto &c : checks)
     if (argc == 2 && !strcmp(argv[1], c.first)) {

@@ -67,6 +67,26 @@ def test_embedding_of_a_bfloat16_table_to_float32(n):
     ref.check(w.grad, want, tol)
 
 
+def test_embed_grad_of_the_most_ids():
+    """2^30 IDs (a gradient of 17 GB): whole numbers whose sums are exact."""
+    n, V, D, rows = 1 << 30, 1 << 16, 8, 1 << 14
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    ids = torch.arange(V, dtype=torch.int32, device=device()).repeat(rows)
+    # position t = (j, v): (v + j) % 5 - 1, and the column
+    j = torch.arange(rows, device=device(), dtype=torch.int32)[:, None]
+    v = torch.arange(V, device=device(), dtype=torch.int32)
+    g = torch.empty((n, D), dtype=BF16, device=device())
+    want = torch.zeros((V, D), device=device())
+    for a in range(0, rows, 1024):
+        x = ((v + j[a:a + 1024]) % 5 - 1).to(BF16)[:, :, None] * torch.arange(1, D + 1, device=device()).to(BF16)
+        g.view(rows, V, D)[a:a + 1024] = x
+        want += x.float().sum(0)
+    st = status()
+    got = lm.embed_grad(g, ids, V, status=st)
+    assert torch.equal(got, want) and int(st.item()) == 0
+
+
 # ---- logits: queues that overflow, wide workgroups with a queue ----------------------
 def check_logits(V, lists, lt, ot, seed):
     """lists: for each row its prompt, its generated IDs and how many biases."""

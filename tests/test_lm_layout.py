@@ -7,6 +7,9 @@ import subprocess
 
 import pytest
 
+from byte_level_bpe_pretokenize_amd import _lib
+
+P = 16  # a pointer that no check follows
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SAN = ["-fsanitize=address,undefined", "-fno-sanitize-recover=all", "-fno-omit-frame-pointer",
        "-g", "-O1"]
@@ -26,10 +29,23 @@ def driver(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("check", ["layout", "divisor", "variant", "logits_limit"])
+@pytest.mark.parametrize("check", ["layout", "divisor", "variant", "grad_limit", "logits_limit"])
 def test_layout(driver, check):
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=1:verify_asan_link_order=0",
                UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
     r = subprocess.run([driver, check], capture_output=True, text=True, env=env, timeout=300)
     assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-4000:]
     assert "passed" in r.stdout
+
+
+def test_sizes_in_the_stated_range_are_not_refused():
+    """The host's checks pass sizes up to the header's limits: what comes next is
+    the refusal of a workspace that is too small."""
+    L = _lib.load()
+    for n, V, D in ((1 << 30, 100, 8), (1 << 30, _lib.MAX_ROWS, 512), (1 << 30, 100, 1536),
+                    (1 << 23, 1000, _lib.MAX_WIDTH - 512)):
+        assert L.bpe_embed_grad_workspace_bytes(n, V, D) > 16 * n
+        assert L.bpe_embed_grad(P, 1, D, P, n, V, D, 1.0, -1, 0, P, 0, D, P, 0, P, None) == _lib.BPE_EWORKSPACE
+    for n, V, D in ((1 << 30, 100, 1537), (1 << 24, 1000, _lib.MAX_WIDTH)):
+        assert L.bpe_embed_grad_workspace_bytes(n, V, D) == 0
+        assert L.bpe_embed_grad(P, 1, D, P, n, V, D, 1.0, -1, 0, P, 0, D, P, 1 << 50, P, None) == _lib.BPE_EINVAL
