@@ -39,7 +39,8 @@ extern "C" {
 size_t bpe_embed_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t width, int weight_type,
                                  int out_type) {
   if (!type_ok(weight_type) || !type_ok(out_type) || n_ids <= 0 || n_ids > BPE_MAX_IDS ||
-      !table_ok(n_rows, width) || !by_sorted_ids(n_ids, n_rows, width, weight_type, out_type))
+      !table_ok(n_rows, width) || !embed_fits(n_ids, width, out_type) ||
+      !by_sorted_ids(n_ids, n_rows, width, weight_type, out_type))
     return 0;
   return grad_layout(n_ids, n_rows, width).touched;  // what the sort needs comes first
 }
@@ -53,7 +54,7 @@ int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t wid
       pad_id < -1 || !d_status || (n_ids > 0 && (!d_weight || !d_ids || !d_out)))
     return BPE_EINVAL;
   if (n_ids == 0) return BPE_OK;
-  if (n_ids * (width < 8 ? width : (width + 3) / 4) > kMaxGrid * kEmbedUnits) return BPE_EINVAL;
+  if (!embed_fits(n_ids, width, out_type)) return BPE_EINVAL;
   EmbedArgs a = {};
   a.weight = d_weight;
   a.ids = d_ids;

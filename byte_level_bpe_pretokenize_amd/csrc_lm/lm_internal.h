@@ -85,6 +85,7 @@ struct GradLayout {
   int32_t sort_tiles, sort_steps, passes, bits, tile, tiles;
 };
 
+bool embed_fits(int64_t n_ids, int64_t width, int ot);
 bool by_sorted_ids(int64_t n_ids, int64_t n_rows, int64_t width, int wt, int ot);
 
 // a.key != nullptr: by sorted IDs, after the sort that `sort` describes.

@@ -16,6 +16,15 @@ size_t place(size_t *at, size_t bytes) {
 
 }  // namespace
 
+// Whether the forward is one launch: vectors of 16 bytes of the output (of one
+// element in rows of less than 8), kEmbedUnits per workgroup of 256 threads.
+// (By sorted IDs a wave has 64 positions and 64 vectors: no more workgroups.)
+bool embed_fits(int64_t n_ids, int64_t width, int ot) {
+  const int64_t per = width < 8 ? 1 : 16 / type_bytes(ot);
+  const int64_t vectors = n_ids * ((width + per - 1) / per);
+  return launch_fits((vectors + kEmbedUnits - 1) / kEmbedUnits, 256);
+}
+
 // Whether the forward goes by sorted IDs: where many IDs read each row of a
 // table whose elements are wider than the output's, so that what the caches
 // lose costs more than storing the rows out of order.  262,144 IDs, float32 to

@@ -68,7 +68,8 @@ size_t bpe_embed_workspace_bytes(int64_t n_ids, int64_t n_rows, int64_t width, i
  * An ID outside [0, n_rows) that is not pad_id gives a row of zeros and sets
  * BPE_STATUS_BAD_ID.  out must not overlap weight.  d_workspace: device
  * scratch, 16-byte aligned, of workspace_bytes >= bpe_embed_workspace_bytes of
- * the same sizes and types (NULL where that is 0).
+ * the same sizes and types (NULL where that is 0).  The rows of out, in whole
+ * 16-byte pieces, take at most 2^34 - 1024 pieces (256 GiB).
  * Returns BPE_OK, BPE_EINVAL, BPE_EWORKSPACE or BPE_EHIP.
  */
 int bpe_embed(const void *d_weight, int weight_type, int64_t n_rows, int64_t width,

@@ -98,6 +98,32 @@ static void variant() {
     }
 }
 
+// A forward that passes the checks has launches of fewer than 2^32 threads, and
+// the header's bound is the one that is checked.
+static void embed_limit() {
+  const int64_t most = ((int64_t)1 << 34) - 1024;
+  int fits = 0, not_ = 0;
+  for (int i = 0; i < 100000; ++i) {
+    const int ot = (int)(rng() % 3);
+    const int64_t n = between(1, BPE_MAX_IDS), size = ot == BPE_F32 ? 4 : 2;
+    int64_t D = between(8, BPE_MAX_WIDTH);
+    if (i % 2) D = std::min<int64_t>(BPE_MAX_WIDTH, std::max<int64_t>(8, most / n * 16 / size + (int64_t)(rng() % 41) - 20));
+    const int64_t vectors = n * ((D * size + 15) / 16);
+    CHECK(embed_fits(n, D, ot) == (vectors <= most));
+    if (!embed_fits(n, D, ot)) {
+      ++not_;
+      continue;
+    }
+    ++fits;
+    CHECK((vectors + kEmbedUnits - 1) / kEmbedUnits * 256 < (int64_t)1 << 32);
+    // by sorted IDs: four waves per workgroup
+    const int64_t E = 16 / size, waves = (n + 63) / 64 * ((D + 64 * E - 1) / (64 * E));
+    CHECK((waves + 3) / 4 * 256 < (int64_t)1 << 32);
+  }
+  CHECK(fits > 1000 && not_ > 1000);
+  for (int64_t D = 1; D < 8; ++D) CHECK(embed_fits(BPE_MAX_IDS, D, BPE_F32));
+}
+
 // A gradient that passes the checks has launches of fewer than 2^32 threads,
 // and the header's bound is the one that is checked.
 static void grad_limit() {
@@ -152,10 +178,9 @@ static void logits_limit() {
 }
 
 int main(int argc, char **argv) {
-  const std::pair<const char *, void (*)()> checks[] = {{"layout", layout}, {"divisor", divisor},
-                                                         {"variant", variant},
-                                                         {"grad_limit", grad_limit},
-                                                         {"logits_limit", logits_limit}};
+  const std::pair<const char *, void (*)()> checks[] = {
+      {"layout", layout},           {"divisor", divisor},       {"variant", variant},
+      {"embed_limit", embed_limit}, {"grad_limit", grad_limit}, {"logits_limit", logits_limit}};
   for (const auto &c : checks)
     if (argc == 2 && !strcmp(argv[1], c.first)) {
       c.second();

@@ -36,6 +36,24 @@ def test_embed_by_sorted_ids_few_lanes(D):
     assert torch.all(gaps(out, 3) == 0)
 
 
+def test_embed_of_the_most_rows():
+    """More than 2^33 pieces of four elements (an output of 71 GB), and workgroups
+    past 2^22."""
+    n, D, V = 953_000_001, 37, 1000
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB")
+    w = randn((V, D), BF16, 1)
+    ids = torch.arange(n, dtype=torch.int32, device=device()) % V
+    st = status()
+    got = lm.embed(w, ids, 0.5, status=st)
+    want = (w.float() * 0.5).to(BF16)
+    whole = n // V
+    for a in range(0, whole, 20000):
+        b = min(whole, a + 20000)
+        assert bool((got[a * V:b * V].view(b - a, V, D) == want).all()), a
+    assert torch.equal(got[whole * V:], want[:n - whole * V]) and int(st.item()) == 0
+
+
 # ---- the gradient by sorted IDs, float32 to half precision ------------------------
 @pytest.mark.parametrize("ot", [BF16, F16])
 @pytest.mark.parametrize("n,V,D", [(2049, 90, 7), (3001, 1500, 72), (6144, 300, 513), (6145, 300, 520),

@@ -29,7 +29,7 @@ def driver(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("check", ["layout", "divisor", "variant", "grad_limit", "logits_limit"])
+@pytest.mark.parametrize("check", ["layout", "divisor", "variant", "embed_limit", "grad_limit", "logits_limit"])
 def test_layout(driver, check):
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=1:verify_asan_link_order=0",
                UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
@@ -42,6 +42,13 @@ def test_sizes_in_the_stated_range_are_not_refused():
     """The host's checks pass sizes up to the header's limits: what comes next is
     the refusal of a workspace that is too small."""
     L = _lib.load()
+    for n, D in ((1 << 30, 64), (1 << 30, 120), ((1 << 27) - 8, 1024)):
+        need = L.bpe_embed_workspace_bytes(n, 100, D, 0, 1)
+        assert need > 16 * n
+        assert L.bpe_embed(P, 0, 100, D, D, P, n, 1.0, -1, P, 1, D, P, need - 1, P, None) == _lib.BPE_EWORKSPACE
+    for n, D in ((1 << 30, 121), (1 << 27, 1024)):
+        assert L.bpe_embed_workspace_bytes(n, 100, D, 0, 1) == 0
+        assert L.bpe_embed(P, 0, 100, D, D, P, n, 1.0, -1, P, 1, D, P, 1 << 50, P, None) == _lib.BPE_EINVAL
     for n, V, D in ((1 << 30, 100, 8), (1 << 30, _lib.MAX_ROWS, 512), (1 << 30, 100, 1536),
                     (1 << 23, 1000, _lib.MAX_WIDTH - 512)):
         assert L.bpe_embed_grad_workspace_bytes(n, V, D) > 16 * n
