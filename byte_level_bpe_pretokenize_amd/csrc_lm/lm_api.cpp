@@ -178,7 +178,7 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
                      int32_t block_size, int64_t *d_slots, int32_t *d_positions,
                      int32_t *d_lengths, int64_t *d_used, void *d_workspace,
                      size_t workspace_bytes, int32_t *d_status, void *hip_stream) {
-  if (n_requests < 0 || n_requests > BPE_MAX_IDS || n_new < 0 || n_new > kMaxGrid * kBlockChunk ||
+  if (n_requests < 0 || n_requests > BPE_MAX_IDS || n_new < 0 || n_new > kBlockMaxNew ||
       n_free < 0 || block_size < 1 || table_width < 0 || table_width > INT32_MAX ||
       !stride_ok(table_stride, table_width) || !d_status || !d_used ||
       (n_new > 0 && n_requests == 0) || (n_free > 0 && !d_free_blocks))

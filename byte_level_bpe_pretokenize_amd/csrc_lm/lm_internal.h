@@ -10,11 +10,8 @@
 
 namespace bpe {
 
-// Workgroups of one launch, at most (a launch has fewer than 2^32 threads, of
-// up to 512 a workgroup).
-constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;
-
-// Whether that many workgroups of so many threads are one launch.
+// Whether that many workgroups of so many threads are one launch (of fewer than
+// 2^32 threads).
 inline bool launch_fits(int64_t groups, int threads) {
   return groups <= (((int64_t)1 << 32) - 1) / threads;
 }
@@ -130,6 +127,7 @@ struct BlockArgs {
 };
 
 constexpr int kBlockChunk = 2048;     // new tokens per workgroup
+constexpr int64_t kBlockMaxNew = ((int64_t)1 << 34) - kBlockChunk;  // (206 GB of outputs)
 constexpr int kBlockGroups = 256;     // groups of requests, at most
 constexpr int kBlockFused = 2048;     // requests that each workgroup sums by itself
 constexpr int kBlockScan = 1024;      // threads of the scan: requests per step

@@ -24,7 +24,8 @@
  *    set the outputs are as stated below, and no access leaves the caller's
  *    buffers.
  *  - Matrices are rows of `width` consecutive elements, `stride` elements
- *    apart (stride >= width).  A pointer need only be aligned to its element.
+ *    apart (width <= stride <= 2^32).  A pointer need only be aligned to its
+ *    element.
  *  - Sums and products are formed in float32 and rounded once, to nearest
  *    even, on the way out.  Results do not depend on scheduling: the same
  *    inputs give the same bits.
@@ -187,6 +188,7 @@ size_t bpe_block_tables_workspace_bytes(int64_t n_requests, int64_t n_new);
  * above INT32_MAX sets BPE_STATUS_BAD_LENGTH: the former counts as 0, and
  * tokens past the latter get slot and position -1.  A token in a block whose
  * table entry is negative gets slot -1.
+ * n_requests <= 2^30, n_new <= 2^34 - 2048.
  * Returns BPE_OK, BPE_EINVAL, BPE_EWORKSPACE or BPE_EHIP.
  */
 int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new,

@@ -56,3 +56,16 @@ def test_sizes_in_the_stated_range_are_not_refused():
     for n, V, D in ((1 << 30, 100, 1537), (1 << 24, 1000, _lib.MAX_WIDTH)):
         assert L.bpe_embed_grad_workspace_bytes(n, V, D) == 0
         assert L.bpe_embed_grad(P, 1, D, P, n, V, D, 1.0, -1, 0, P, 0, D, P, 1 << 50, P, None) == _lib.BPE_EINVAL
+
+
+def test_block_tables_limits():
+    """The header's limits of block tables: (1 << 34) - 2048 new tokens, 1 << 30
+    requests."""
+    L = _lib.load()
+
+    def rc(R, T):
+        return L.bpe_block_tables(P, R, T, P, P, 5, P, 4, 4, 16, P, P, P, P, P, 0, P, None)
+
+    assert rc(1 << 30, (1 << 34) - 2048) == _lib.BPE_EWORKSPACE
+    assert rc((1 << 30) + 1, 10) == _lib.BPE_EINVAL
+    assert rc(1 << 30, (1 << 34) - 2047) == _lib.BPE_EINVAL
