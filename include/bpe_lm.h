@@ -46,7 +46,7 @@ extern "C" {
 
 /* bits of *d_status, next to BPE_STATUS_BAD_ID and BPE_STATUS_BAD_ID_OFFSETS */
 #define BPE_STATUS_NO_BLOCKS 32u     /* more blocks needed than free_blocks holds */
-#define BPE_STATUS_TABLE_FULL 64u    /* a request's length exceeds its row of the block table */
+#define BPE_STATUS_TABLE_FULL 64u    /* a new token lies past its request's row of the block table */
 #define BPE_STATUS_BAD_LENGTH 128u   /* a negative length, or one above its bound */
 #define BPE_STATUS_BAD_MASK_ROW 256u /* a mask row below -1 or not below n_masks */
 #define BPE_STATUS_BAD_BIAS 512u     /* a row's bias IDs do not increase */
@@ -183,8 +183,9 @@ size_t bpe_block_tables_workspace_bytes(int64_t n_requests, int64_t n_new);
  *            ... <= new_off[R] = n_new set BPE_STATUS_BAD_ID_OFFSETS, and the
  *            outputs are not valid.
  * Past the last free block (BPE_STATUS_NO_BLOCKS) table entries and slots are
- * -1; used[0] still counts what is needed.  Tokens past table_width blocks
- * (BPE_STATUS_TABLE_FULL) get slot -1.  A negative cached length or a length
+ * -1; used[0] still counts what is needed.  New tokens past table_width blocks
+ * (BPE_STATUS_TABLE_FULL) get slot -1; a request without new tokens is not
+ * held against the table's width.  A negative cached length or a length
  * above INT32_MAX sets BPE_STATUS_BAD_LENGTH: the former counts as 0, and
  * tokens past the latter get slot and position -1.  A token in a block whose
  * table entry is negative gets slot -1.

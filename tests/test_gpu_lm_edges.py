@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import lm_reference as ref
-from byte_level_bpe_pretokenize_amd import BPEError, lm
+from byte_level_bpe_pretokenize_amd import BPEError, _lib, lm
 
 from gpu_util import device
 from test_gpu_lm import (BF16, F16, F32, blocks_case, check_blocks, dev, gaps, gen, ids_of, randn,
@@ -204,6 +204,21 @@ def test_blocks_past_the_caches(R, most, bs):
     off, c, free, table = blocks_case(R, bs, R, most=most, cached=500)
     assert off[-1] * 12 >= 32 << 20
     assert check_blocks(off, c, free, table, bs) == 0
+
+
+@pytest.mark.parametrize("R", [3, 3000])
+def test_blocks_table_full_is_about_new_tokens(R):
+    """A request of 100 cached tokens in a table of 3 blocks of 16: no bit without
+    new tokens, and one with."""
+    table = np.zeros((R, 3), np.int32)
+    c, new = np.zeros(R, np.int32), np.ones(R, np.int64)
+    c[1], new[1] = 100, 0
+    off = np.concatenate([[0], np.cumsum(new)])
+    free = np.arange(1, R + 1, dtype=np.int32)
+    assert check_blocks(off, c, free, table, 16) == 0
+    new[1] = 1
+    off = np.concatenate([[0], np.cumsum(new)])
+    assert check_blocks(off, c, free, table, 16) == _lib.STATUS_TABLE_FULL
 
 
 # ---- another stream -------------------------------------------------------------------
