@@ -414,15 +414,23 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
                   used, workspace, status))
     L = _lib.load()
     st = _status(status, dev)
-    given = [t for t in (table, slots, positions, lengths, used) if t is not None]
+    filled = [table]  # the caller's tensors
     if slots is None:
         slots = new_off.new_empty(n_new)
+    else:
+        filled.append(slots)
     if positions is None:
         positions = cached.new_empty(n_new)
+    else:
+        filled.append(positions)
     if lengths is None:
         lengths = cached.new_empty(R)
+    else:
+        filled.append(lengths)
     if used is None:
         used = new_off.new_empty(1)
+    else:
+        filled.append(used)
     if workspace is None:
         w_bytes = L.bpe_block_tables_workspace_bytes(R, n_new)
         workspace = torch.empty(w_bytes, dtype=torch.uint8, device=dev) if w_bytes else None
@@ -433,6 +441,6 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
                             lengths.data_ptr(), used.data_ptr(),
                             None if workspace is None else workspace.data_ptr(), w_bytes,
                             st.data_ptr(), _stream(dev))
-    _modified(given)
+    _modified(filled)
     _end("bpe_block_tables", rc, st if status is None else None)
     return slots, positions, lengths, used
