@@ -104,17 +104,24 @@ struct FillShared {
 // tokens per thread and step, so that a wave stores whole lines: where they are
 // one request's and in new blocks, one read of the request (from LDS), one
 // multiply-high for the block and one load of its number and the next one's.
-// The few pairs that are not (two requests', a block that was partly filled,
-// the ends of the table and of the free blocks) are listed and done one token
-// per thread afterwards; done in place they cost every wave that path.  The
+// The pairs that are not (two requests', a block that was partly filled, the
+// ends of the table and of the free blocks) are listed and done one token per
+// thread afterwards; done in place they cost every wave that path.  They are few
+// where requests bring many tokens to an empty cache, all of them in a step of
+// one token per request, and in between where blocks are long (65,536 requests
+// of 190 tokens: 34 us with blocks of 16 and nothing cached, 40 with up to 1,000
+// tokens each, 44 with those in blocks of 128).  The
 // token at a block's first place in the cache also enters the block into the
 // table: a new block's first place always belongs to a new token.  What bounds
 // it is the chain of dependent loads in each workgroup, kept to four (the
 // chunk's request, the requests, their groups, the blocks of all tokens), and
-// the arithmetic: 31 us for 12.5 M tokens of 65,536 requests (157 MB, 5.1 TB/s;
-// stores alone of those bytes take 22 us).
+// the arithmetic: 31 us for 12.5 M tokens of 65,536 requests after 4 to 5 for
+// their sums (157 MB in 34.7 us, 4.5 TB/s; stores alone of those bytes take 22).
 // FUSED (R <= kBlockFused): each workgroup sums the requests' needs itself, one
-// launch in all.
+// launch in all.  That is ahead while the workgroups are few: 2,048 requests
+// with 20,480 or 198,656 new tokens take 13.0 us (two launches 16.5), with 2.0 M
+// tokens 19.1 (17.7), and with 12 M, where 5,860 workgroups sum the same
+// requests, 65 (32).  The limit knows the requests alone.
 template <bool FUSED, bool STREAM>
 __global__ void __launch_bounds__(BWG, FUSED ? 4 : 8) k_block_fill(BlockArgs a) {
   __shared__ FillShared s;

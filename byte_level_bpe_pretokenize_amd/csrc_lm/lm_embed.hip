@@ -13,18 +13,21 @@ namespace {
 // elements a second time with the same values.  U vectors per thread: their
 // ID loads, then their row loads, are in flight together.  E is 16 bytes of the
 // output, so that a wave's stores are whole lines.  BIG: the output is stored
-// past the caches (float32 rows of 4,096 to bfloat16, 262,144 IDs: 691 us
-// without, 659 with).
-// Bound by memory: those 2.57 GB (each row of the table read once) move at 3.9
-// TB/s, where a copy of 8 GiB makes 4.7; what is missing are rows that fell out
-// of the L2s and are read again (2.6 GB instead of 0.4).  Column slabs, one per
-// XCD or one after another, keep more rows in the caches but store shorter
-// runs: 648 to 788 us.
+// past the caches (bfloat16 rows of 4,096 of a table of 32,256, 262,144 IDs:
+// 552 us without, 472 with; 32,768 IDs: 75 and 62; 65,536 of a float32 table to
+// bfloat16: 177 and 167).
+// Bound by memory: the 2.41 GB of the largest of these (each row of the table
+// read once) move at 5.1 TB/s.  Rows that fell out of the L2s and are read
+// again come on top of them; where the table's elements are wider than the
+// output's those cost most, and large batches of such go by sorted IDs
+// (k_embed_runs) instead: 659 us here for the same IDs of a float32 table.
+// Column slabs, one per XCD or one after another, keep more of these rows in
+// the caches but store shorter runs: 648 to 788 us.
 // 64 IDs take 3.2 us.
 template <typename TI, typename TO, int E, int U, bool BIG>
 __global__ void __launch_bounds__(256) k_embed(EmbedArgs a) {
   const int tid = threadIdx.x;
-    const int64_t base = (int64_t)blockIdx.x * (256 * U);
+  const int64_t base = (int64_t)blockIdx.x * (256 * U);
   const int64_t t0 = base / a.units;
   const uint32_t u0 = (uint32_t)(base - t0 * a.units);
   int32_t id[U];
@@ -494,10 +497,19 @@ __global__ void __launch_bounds__(256) k_grad_sum(GradArgs a) {
 // ID's positions in order and adds up their rows: up to kRowsAhead rows by one
 // wave per slab, more by all eight waves, every eighth row each, joined in
 // order.  The other workgroups mark which of their rows occur and write zeros
-// to the rest.  One launch instead of four, which is what such a call costs:
-// 2,048 IDs of 768 rows of 512 take 9 us, most of it the chain of dependent
-// loads (the IDs, the rows of the most frequent ID), and 27 with the sort.  The
-// work grows with the square of n_ids: 4,096 IDs take 37 us, with the sort 28.
+// to the rest.  One launch instead of three or four, which is what such a call
+// costs: 2,048 IDs of 768 rows of 512 take 10 us, most of it the chain of
+// dependent loads (the IDs, the rows of the most frequent ID), and 20 by sorted
+// IDs.  Every workgroup reads all IDs again, so the work grows with their square
+// and with the width.  The limit kGradDirect fits narrow tables, and is past the
+// even point of wide ones; in us, this and the sort, bfloat16 rows:
+//                   1,024 IDs     2,048 IDs     4,096 IDs
+//   768 x 512          9   19       11   20       21   22
+//   768 x 4,096       17   21       30   24       71   31
+//   768 x 8,192       29   24       56   29      138   37
+//   32,256 x 512      12   29       16   30       29   32
+//   32,256 x 4,096    64   68       80   70      126   76
+//   32,256 x 8,192   126  119      157  123      244  133
 constexpr int kDirectSlabs = 2;
 constexpr int kDirectZero = 32;  // rows of the table per workgroup of zeros
 

@@ -38,8 +38,9 @@ struct EmbedArgs {
 
 // ---- the embedding's gradient ----------------------------------------------
 // The IDs are sorted (a stable radix sort of at most kDigitBits bits per pass,
-// in at most kSortTiles tiles, whose counts every workgroup reads); the sorted list is cut into tiles of `tile` IDs, one
-// wave per tile and 64 vectors of columns.
+// in at most kSortTiles tiles, whose counts every workgroup reads); the sorted
+// list is cut into tiles of `tile` IDs, one wave per tile and 64 vectors of
+// columns.
 constexpr int kEmbedUnits = 1024;  // vectors per workgroup of the forward
 constexpr int kZeroRows = 16;      // rows of the table per workgroup of zeros
 constexpr int kGradTile = 256;     // IDs per tile of the sums, at most
