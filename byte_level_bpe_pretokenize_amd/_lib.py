@@ -21,7 +21,8 @@ SYMBOLS = (
 # every symbol include/bpe_lm.h declares
 LM_SYMBOLS = (
     "bpe_embed_workspace_bytes", "bpe_embed", "bpe_embed_grad_workspace_bytes", "bpe_embed_grad", "bpe_process_logits",
-    "bpe_block_tables_workspace_bytes", "bpe_block_tables",
+    "bpe_block_tables_workspace_bytes", "bpe_block_tables", "bpe_cache_write", "bpe_cache_read",
+    "bpe_verify_drafts", "bpe_distill", "bpe_distill_grad",
 )
 
 BPE_OK, BPE_EINVAL, BPE_EMERGES, BPE_EIDMAP, BPE_EWORKSPACE, BPE_EHIP, BPE_ENOMEM, BPE_ENOTSUP, \
@@ -31,9 +32,12 @@ STATUS_BAD_DOC_OFFSETS, STATUS_IDS_CAPACITY, STATUS_BAD_ID, STATUS_BYTES_CAPACIT
     STATUS_BAD_ID_OFFSETS = 1, 2, 4, 8, 16
 STATUS_NO_BLOCKS, STATUS_TABLE_FULL, STATUS_BAD_LENGTH, STATUS_BAD_MASK_ROW, STATUS_BAD_BIAS = \
     32, 64, 128, 256, 512
+STATUS_BAD_SLOT, STATUS_NOT_FINITE, STATUS_NO_TOKEN = 1024, 2048, 4096
 F32, BF16, F16 = 0, 1, 2
+E4M3, INT8, UINT4 = 0, 1, 2
 MAX_WIDTH = 1 << 17
 MAX_ROWS = 1 << 26
+MAX_HEADS = MAX_DIM = MAX_TOP = 1024
 OP_ENCODE, OP_DECODE = 0, 1
 MAX_MERGES = 1 << 20
 MAX_ID = (1 << 24) - 1
@@ -55,6 +59,15 @@ class LogitsArgs(C.Structure):
         ("mask_row", C.c_void_p),
         ("out", C.c_void_p), ("out_stride", C.c_int64), ("status", C.c_void_p),
         ("logits_type", C.c_int32), ("out_type", C.c_int32),
+    ]
+
+
+class Cache(C.Structure):
+    """bpe_cache of include/bpe_lm.h."""
+    _fields_ = [
+        ("codes", C.c_void_p), ("scales", C.c_void_p),
+        ("n_slots", C.c_int64), ("codes_stride", C.c_int64), ("scales_stride", C.c_int64),
+        ("heads", C.c_int32), ("dim", C.c_int32), ("group", C.c_int32), ("format", C.c_int32),
     ]
 
 
@@ -127,5 +140,15 @@ def load() -> C.CDLL:
     L.bpe_block_tables_workspace_bytes.restype = sz
     L.bpe_block_tables.argtypes = [p, i64, i64, p, p, i64, p, i64, i64, i32, p, p, p, p, p, sz, p, p]
     L.bpe_block_tables.restype = i32
+    L.bpe_cache_write.argtypes = [C.POINTER(Cache), p, i32, i64, i64, i64, p, p, p]
+    L.bpe_cache_write.restype = i32
+    L.bpe_cache_read.argtypes = [C.POINTER(Cache), p, i64, i64, i64, i32, p, p, i64, p, i32, i64, i64, p, p]
+    L.bpe_cache_read.restype = i32
+    L.bpe_verify_drafts.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, i64, p, p, p, p, p, p]
+    L.bpe_verify_drafts.restype = i32
+    L.bpe_distill.argtypes = [p, i32, i64, i64, i64, p, i64, p, i32, i64, i64, f32, p, p, p, p]
+    L.bpe_distill.restype = i32
+    L.bpe_distill_grad.argtypes = [p, i32, i64, i64, i64, p, i64, p, i32, i64, i64, p, p, f32, p, i32, i64, p, p]
+    L.bpe_distill_grad.restype = i32
     _lib = L
     return L

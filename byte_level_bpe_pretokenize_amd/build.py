@@ -17,7 +17,8 @@ SOURCES = [os.path.join(CSRC, f)
                      "bpe_api.cpp", "bpe_tables.cpp", "bpe_text.cpp")]
 # the operators on token IDs (include/bpe_lm.h)
 SOURCES += [os.path.join(PKG, "csrc_lm", f)
-            for f in ("lm_embed.hip", "lm_logits.hip", "lm_blocks.hip", "lm_api.cpp", "lm_layout.cpp")]
+            for f in ("lm_embed.hip", "lm_logits.hip", "lm_blocks.hip", "lm_cache.hip",
+                      "lm_verify.hip", "lm_distill.hip", "lm_api.cpp", "lm_layout.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

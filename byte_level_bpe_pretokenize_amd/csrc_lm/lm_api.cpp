@@ -32,6 +32,16 @@ bool stride_ok(int64_t stride, int64_t width) {
   return stride >= width && stride <= ((int64_t)1 << 32);
 }
 
+bool distill_ok(int student_type, int64_t n_rows, int64_t vocab, int64_t student_stride,
+                int64_t ids_stride, int teacher_type, int64_t teacher_stride, int64_t top,
+                float temperature) {
+  return type_ok(student_type) && type_ok(teacher_type) && n_rows >= 0 &&
+         launch_fits(n_rows, kDistillWide) && vocab >= 1 && vocab <= BPE_MAX_ROWS &&
+         stride_ok(student_stride, vocab) && top >= 0 && top <= BPE_MAX_TOP &&
+         stride_ok(ids_stride, top) && stride_ok(teacher_stride, top) && temperature >= 0x1p-20f &&
+         temperature <= 0x1p20f;
+}
+
 }  // namespace
 
 extern "C" {
@@ -215,6 +225,153 @@ int bpe_block_tables(const int64_t *d_new_off, int64_t n_requests, int64_t n_new
   a.group_log2 = 10;
   while (((n_requests - 1) >> a.group_log2) + 1 > kBlockGroups) ++a.group_log2;
   return launch_blocks(a, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
+}
+
+int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t n,
+                    int64_t token_stride, int64_t head_stride, const int64_t *d_slots,
+                    int32_t *d_status, void *hip_stream) {
+  if (!cache || !type_ok(x_type) || !cache_ok(*cache) ||
+      !cache_tokens_ok(*cache, n, token_stride, head_stride) || !d_status ||
+      (n > 0 && (!d_x || !d_slots)))
+    return BPE_EINVAL;
+  if (n == 0) return BPE_OK;
+  CacheArgs a = {};
+  a.c = *cache;
+  a.n = n;
+  a.t_stride = token_stride;
+  a.h_stride = head_stride;
+  a.status = d_status;
+  a.x = d_x;
+  a.slots = d_slots;
+  cache_shape(&a, true);
+  if (!launch_fits(cache_workgroups(a), kCacheThreads)) return BPE_EINVAL;
+  return launch_cache_write(a, x_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
+}
+
+int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_requests,
+                   int64_t table_width, int64_t table_stride, int32_t block_size,
+                   const int64_t *d_off, const int32_t *d_start, int64_t n, void *d_out,
+                   int out_type, int64_t token_stride, int64_t head_stride, int32_t *d_status,
+                   void *hip_stream) {
+  if (!cache || !type_ok(out_type) || !cache_ok(*cache) ||
+      !cache_tokens_ok(*cache, n, token_stride, head_stride) || n_requests < 0 ||
+      n_requests > BPE_MAX_IDS || table_width < 0 || table_width > INT32_MAX ||
+      !stride_ok(table_stride, table_width) || block_size < 1 || !d_status || (n > 0 && !d_out) ||
+      (n_requests > 0 && (!d_off || (table_width > 0 && !d_table))))
+    return BPE_EINVAL;
+  if (n == 0 || n_requests == 0) return BPE_OK;
+  CacheArgs a = {};
+  a.c = *cache;
+  a.n = n;
+  a.t_stride = token_stride;
+  a.h_stride = head_stride;
+  a.status = d_status;
+  a.out = d_out;
+  a.table = d_table;
+  a.start = d_start;
+  a.off = d_off;
+  a.R = n_requests;
+  a.width = table_width;
+  a.stride = table_stride;
+  a.bs = divisor(block_size);
+  cache_shape(&a, false);
+  if (!launch_fits(cache_workgroups(a), kCacheThreads)) return BPE_EINVAL;
+  return launch_cache_read(a, out_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
+}
+
+int bpe_verify_drafts(const void *d_target, int prob_type, int64_t n_rows, int64_t vocab,
+                      int64_t target_stride, const void *d_draft, int64_t draft_stride,
+                      const int32_t *d_draft_ids, const int64_t *d_row_off, int64_t n_requests,
+                      const float *d_accept, const float *d_sample, int32_t *d_tokens,
+                      int32_t *d_counts, int32_t *d_status, void *hip_stream) {
+  if (!type_ok(prob_type) || n_rows < 0 || n_rows > BPE_MAX_IDS || vocab < 1 ||
+      vocab > BPE_MAX_ROWS || !stride_ok(target_stride, vocab) ||
+      (d_draft && !stride_ok(draft_stride, vocab)) || n_requests < 0 ||
+      !launch_fits(n_requests, kVerifyThreads) || !d_status ||
+      (n_rows > 0 && (!d_target || !d_draft_ids || !d_accept || !d_tokens)) ||
+      (n_requests > 0 && (!d_row_off || !d_sample || !d_counts)))
+    return BPE_EINVAL;
+  if (n_requests == 0) return BPE_OK;
+  VerifyArgs a = {};
+  a.target = d_target;
+  a.draft = d_draft;
+  a.n_rows = n_rows;
+  a.vocab = vocab;
+  a.t_stride = target_stride;
+  a.d_stride = draft_stride;
+  a.ids = d_draft_ids;
+  a.off = d_row_off;
+  a.R = n_requests;
+  a.accept = d_accept;
+  a.sample = d_sample;
+  a.tokens = d_tokens;
+  a.counts = d_counts;
+  a.status = d_status;
+  return launch_verify(a, prob_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
+}
+
+int bpe_distill(const void *d_student, int student_type, int64_t n_rows, int64_t vocab,
+                int64_t student_stride, const int32_t *d_ids, int64_t ids_stride,
+                const void *d_teacher, int teacher_type, int64_t teacher_stride, int64_t top,
+                float temperature, float *d_losses, float *d_stats, int32_t *d_status,
+                void *hip_stream) {
+  if (!distill_ok(student_type, n_rows, vocab, student_stride, ids_stride, teacher_type,
+                  teacher_stride, top, temperature) ||
+      !d_status || (n_rows > 0 && (!d_student || !d_losses || !d_stats || (top > 0 && (!d_ids || !d_teacher)))))
+    return BPE_EINVAL;
+  if (n_rows == 0) return BPE_OK;
+  DistillArgs a = {};
+  a.student = d_student;
+  a.teacher = d_teacher;
+  a.rows = n_rows;
+  a.vocab = vocab;
+  a.s_stride = student_stride;
+  a.t_stride = teacher_stride;
+  a.ids = d_ids;
+  a.i_stride = ids_stride;
+  a.top = (int32_t)top;
+  a.temperature = temperature;
+  a.losses = d_losses;
+  a.stats = d_stats;
+  a.status = d_status;
+  return launch_distill(a, student_type, teacher_type, (hipStream_t)hip_stream) == hipSuccess
+             ? BPE_OK
+             : BPE_EHIP;
+}
+
+int bpe_distill_grad(const void *d_student, int student_type, int64_t n_rows, int64_t vocab,
+                     int64_t student_stride, const int32_t *d_ids, int64_t ids_stride,
+                     const void *d_teacher, int teacher_type, int64_t teacher_stride, int64_t top,
+                     const float *d_stats, const float *d_dloss, float temperature, void *d_grad,
+                     int grad_type, int64_t grad_stride, int32_t *d_status, void *hip_stream) {
+  if (!distill_ok(student_type, n_rows, vocab, student_stride, ids_stride, teacher_type,
+                  teacher_stride, top, temperature) ||
+      !type_ok(grad_type) || !stride_ok(grad_stride, vocab) || !d_status ||
+      (n_rows > 0 && (!d_student || !d_stats || !d_dloss || !d_grad || (top > 0 && (!d_ids || !d_teacher)))))
+    return BPE_EINVAL;
+  if (d_grad && d_grad == d_student && (grad_type != student_type || grad_stride != student_stride))
+    return BPE_EINVAL;
+  if (n_rows == 0) return BPE_OK;
+  if (!distill_grad_fits(n_rows, vocab)) return BPE_EINVAL;
+  DistillArgs a = {};
+  a.student = d_student;
+  a.teacher = d_teacher;
+  a.rows = n_rows;
+  a.vocab = vocab;
+  a.s_stride = student_stride;
+  a.t_stride = teacher_stride;
+  a.ids = d_ids;
+  a.i_stride = ids_stride;
+  a.top = (int32_t)top;
+  a.temperature = temperature;
+  a.in_stats = d_stats;
+  a.dloss = d_dloss;
+  a.grad = d_grad;
+  a.g_stride = grad_stride;
+  a.status = d_status;
+  return launch_distill_grad(a, student_type, teacher_type, grad_type, (hipStream_t)hip_stream) == hipSuccess
+             ? BPE_OK
+             : BPE_EHIP;
 }
 
 }  // extern "C"

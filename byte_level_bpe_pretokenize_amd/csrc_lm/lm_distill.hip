@@ -1,0 +1,279 @@
+// lm_distill.hip -- the divergence of a student's distribution from a teacher's
+// over its top tokens, and its gradient.
+#include <float.h>
+
+#include "lm_device.h"
+
+namespace bpe {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// A running maximum and the sum of exp((x - maximum) / T) below it, k = log2(e) /
+// T.  It starts at the lowest finite value: a -infinity adds 0 to that, and a row
+// of lowest values is still a distribution.  A NaN or +infinity makes the sum NaN.
+struct Soft {
+  float m, s;
+};
+constexpr Soft kNothing = {-FLT_MAX, 0.f};
+
+__device__ __forceinline__ float power(float x, float k) { return __builtin_amdgcn_exp2f(x * k); }
+
+// The wave's, in every lane.
+__device__ __forceinline__ Soft wave_soft(Soft x, float k) {
+  float m = x.m;
+  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+  x.s = wave_sum(x.s * power(x.m - m, k));
+  x.m = m;
+  return x;
+}
+
+// An entry of a teacher's row: its token's place, or -1.
+struct Entry {
+  int32_t id;
+  float t;
+};
+template <typename TT>
+__device__ __forceinline__ Entry load_entry(const DistillArgs &a, int64_t n, int j) {
+  Entry x = {-1, -INFINITY};
+  if (j < a.top) {
+    x.id = a.ids[n * a.i_stride + j];
+    x.t = (float)((const TT *)a.teacher)[n * a.t_stride + j];
+  }
+  return x;
+}
+
+// A workgroup per row: one pass over the logits with a running maximum and sum
+// per thread, joined over the workgroup; the listed logits are gathered before.
+// With e_j = exp((t_j - largest t) / T), the loss is
+//   T^2 (sum e_j ((t_j - largest t) - (z_j - largest z)) / (T sum e_j) + log sum z - log sum t)
+// whose last terms and sum are in 64 bits: it is the difference of values larger
+// than itself where the student is near the teacher.
+template <typename TS, typename TT, int NT>
+__global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
+  constexpr int E = 16 / sizeof(TS), U = 4, STEP = NT * E;
+  constexpr int W = NT / 64;
+  __shared__ Soft soft_z[W], soft_t[W];
+  __shared__ double terms[W];
+  const int tid = threadIdx.x, lane = lane_id(), wave = wave_id();
+  const int64_t n = blockIdx.x;
+  const TS *z = (const TS *)a.student + n * a.s_stride;
+  const int V = (int)a.vocab;
+  const float k = kLog2e / a.temperature;
+  uint32_t status = 0;
+  auto valid = [&](const Entry &x) { return x.id >= 0 && x.id < V; };
+  const Entry first = load_entry<TT>(a, n, tid);
+  const float z_first = valid(first) ? (float)z[first.id] : 0.f;
+  Soft x = kNothing;
+  auto add = [&](const Vec<TS, E> &v) {
+    float m = x.m;
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, (float)v.v[e]);
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += power((float)v.v[e] - m, k);
+    x.s = x.s * power(x.m - m, k) + s;
+    x.m = m;
+  };
+  int v = 0;
+  for (; v + STEP * U <= V; v += STEP * U) {
+    Vec<TS, E> y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = load_vec<TS, E>(z + v + u * STEP + tid * E);
+#pragma unroll
+    for (int u = 0; u < U; ++u) add(y[u]);
+  }
+  for (v += tid * E; v < V; v += STEP) {
+    Vec<TS, E> y;
+    if (v + E <= V) {
+      y = load_vec<TS, E>(z + v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) y.v[e] = v + e < V ? z[v + e] : (TS)-INFINITY;
+    }
+    add(y);
+  }
+  Soft t = kNothing;
+  for (int j = tid; j < a.top; j += NT) {
+    const Entry y = j == tid ? first : load_entry<TT>(a, n, j);
+    if (y.id < -1 || y.id >= V) status |= BPE_STATUS_BAD_ID;
+    if (!valid(y)) continue;
+    const float m = fmaxf(t.m, y.t);
+    t.s = t.s * power(t.m - m, k) + power(y.t - m, k);
+    t.m = m;
+  }
+  x = wave_soft(x, k);
+  t = wave_soft(t, k);
+  if (lane == 0) {
+    soft_z[wave] = x;
+    soft_t[wave] = t;
+  }
+  __syncthreads();
+  if (W > 1) {
+    x = lane < W ? soft_z[lane] : kNothing;
+    t = lane < W ? soft_t[lane] : kNothing;
+    x = wave_soft(x, k);
+    t = wave_soft(t, k);
+  }
+  const double by = 1.0 / (double)a.temperature;
+  double sum = 0.0;
+  for (int j = tid; j < a.top; j += NT) {
+    const Entry y = j == tid ? first : load_entry<TT>(a, n, j);
+    if (!valid(y)) continue;
+    const float zj = j == tid ? z_first : (float)z[y.id];
+    const float e = power(y.t - t.m, k);
+    if (e != 0.f) sum += (double)e * (((double)y.t - t.m) - ((double)zj - x.m));
+  }
+  sum = wave_sum(sum);
+  if (lane == 0) terms[wave] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    sum = 0.0;
+    for (int w = 0; w < W; ++w) sum += terms[w];
+    const bool some = x.s != 0.f && t.s != 0.f;
+    const double T = a.temperature;
+    a.losses[n] = some ? (float)(T * T * (sum * by / t.s + log((double)x.s) - log((double)t.s))) : 0.f;
+    float *o = a.stats + n * 4;
+    o[0] = x.m;
+    o[1] = x.s;
+    o[2] = t.m;
+    o[3] = t.s;
+  }
+  if (status) atomicOr(a.status, (int32_t)status);
+}
+
+// A workgroup per row and slab of logits: all of them as if nothing were listed,
+// then the listed ones of the slab again.  (Few are listed: asked for at every
+// logit they would cost more.)  A token listed twice gets the same value from
+// both entries: each adds up all of the token's, in their order.
+template <typename TS, typename TT, typename TG>
+__global__ void __launch_bounds__(kDistillThreads) k_distill_grad(DistillArgs a) {
+  constexpr int NT = kDistillThreads, S = kDistillSlab;
+  constexpr int E = sizeof(TS) == 2 && sizeof(TG) == 2 ? 8 : 4;
+  constexpr int U = 4;
+  constexpr int PER = BPE_MAX_TOP / NT;
+  __shared__ int32_t ids[BPE_MAX_TOP];
+  __shared__ float parts[BPE_MAX_TOP];
+  const int tid = threadIdx.x;
+  const uint32_t slabs = (uint32_t)((a.vocab + S - 1) / S);
+  const uint32_t row = blockIdx.x / slabs, slab = blockIdx.x - row * slabs;
+  const int64_t n = row;
+  const int v0 = (int)(slab * S);
+  const int count = (int)min<int64_t>(S, a.vocab - v0);
+  const TS *z = (const TS *)a.student + n * a.s_stride + v0;
+  TG *g = (TG *)a.grad + n * a.g_stride + v0;
+  const float zm = a.in_stats[n * 4], zs = a.in_stats[n * 4 + 1];
+  const float tm = a.in_stats[n * 4 + 2], ts = a.in_stats[n * 4 + 3];
+  const bool some = zs != 0.f && ts != 0.f;
+  const float k = kLog2e / a.temperature;
+  const float c = some ? a.dloss[n] * a.temperature : 0.f;
+  const float by_zs = 1.f / zs, by_ts = 1.f / ts;
+  auto share = [&](float x) { return power(x - zm, k) * by_zs; };
+  // this thread's entries in the slab: their places and logits
+  int at[PER];
+  float zj[PER];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int j = tid + i * NT;
+    at[i] = -1;
+    if (j < a.top) {
+      const Entry y = load_entry<TT>(a, n, j);
+      bad |= y.id < -1 || y.id >= a.vocab;
+      ids[j] = y.id;
+      parts[j] = y.id >= 0 ? power(y.t - tm, k) * by_ts : 0.f;
+      const uint32_t p = (uint32_t)y.id - (uint32_t)v0;
+      if (some && p < (uint32_t)count) {
+        at[i] = (int)p;
+        zj[i] = (float)z[p];
+      }
+    }
+  }
+  if (bad && slab == 0) atomicOr(a.status, BPE_STATUS_BAD_ID);
+  auto gradient = [&](const Vec<TS, E> &x) {
+    Vec<TG, E> y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y.v[e] = from_f32<TG>(some ? c * share((float)x.v[e]) : 0.f);
+    return y;
+  };
+  int v = 0;
+  for (; v + NT * E * U <= count; v += NT * E * U) {
+    Vec<TS, E> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = load_vec<TS, E>(z + v + (u * NT + tid) * E);
+    if (v == 0) __syncthreads();  // (the listed logits are read before any is overwritten)
+#pragma unroll
+    for (int u = 0; u < U; ++u) store_vec<TG, E>(g + v + (u * NT + tid) * E, gradient(x[u]));
+  }
+  if (v == 0) __syncthreads();
+  for (v += tid * E; v < count; v += NT * E) {
+    if (v + E <= count) {
+      store_vec<TG, E>(g + v, gradient(load_vec<TS, E>(z + v)));
+    } else {
+      for (int e = v; e < count; ++e) g[e] = from_f32<TG>(some ? c * share((float)z[e]) : 0.f);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (at[i] < 0) continue;
+    float p = 0.f;
+    for (int j = 0; j < a.top; ++j)
+      if (ids[j] == v0 + at[i]) p += parts[j];
+    g[at[i]] = from_f32<TG>(c * (share(zj[i]) - p));
+  }
+}
+
+template <typename TS, typename TT>
+hipError_t distill_launch(const DistillArgs &a, hipStream_t stream) {
+  if (a.rows < 1024)
+    hipLaunchKernelGGL((k_distill<TS, TT, kDistillWide>), dim3((unsigned)a.rows), dim3(kDistillWide), 0,
+                       stream, a);
+  else
+    hipLaunchKernelGGL((k_distill<TS, TT, kDistillThreads>), dim3((unsigned)a.rows),
+                       dim3(kDistillThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <typename TS>
+hipError_t distill_as(const DistillArgs &a, int tt, hipStream_t stream) {
+  if (tt == BPE_F32) return distill_launch<TS, float>(a, stream);
+  if (tt == BPE_BF16) return distill_launch<TS, bf16_t>(a, stream);
+  return distill_launch<TS, f16_t>(a, stream);
+}
+
+template <typename TS, typename TT, typename TG>
+hipError_t grad_launch(const DistillArgs &a, hipStream_t stream) {
+  const int64_t groups = (a.vocab + kDistillSlab - 1) / kDistillSlab * a.rows;
+  hipLaunchKernelGGL((k_distill_grad<TS, TT, TG>), dim3((unsigned)groups), dim3(kDistillThreads), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+template <typename TS, typename TT>
+hipError_t grad_from(const DistillArgs &a, int gt, hipStream_t stream) {
+  if (gt == BPE_F32) return grad_launch<TS, TT, float>(a, stream);
+  if (gt == BPE_BF16) return grad_launch<TS, TT, bf16_t>(a, stream);
+  return grad_launch<TS, TT, f16_t>(a, stream);
+}
+template <typename TS>
+hipError_t grad_as(const DistillArgs &a, int tt, int gt, hipStream_t stream) {
+  if (tt == BPE_F32) return grad_from<TS, float>(a, gt, stream);
+  if (tt == BPE_BF16) return grad_from<TS, bf16_t>(a, gt, stream);
+  return grad_from<TS, f16_t>(a, gt, stream);
+}
+
+}  // namespace
+
+hipError_t launch_distill(const DistillArgs &a, int st, int tt, hipStream_t stream) {
+  if (st == BPE_F32) return distill_as<float>(a, tt, stream);
+  if (st == BPE_BF16) return distill_as<bf16_t>(a, tt, stream);
+  return distill_as<f16_t>(a, tt, stream);
+}
+
+hipError_t launch_distill_grad(const DistillArgs &a, int st, int tt, int gt, hipStream_t stream) {
+  if (st == BPE_F32) return grad_as<float>(a, tt, gt, stream);
+  if (st == BPE_BF16) return grad_as<bf16_t>(a, tt, gt, stream);
+  return grad_as<f16_t>(a, tt, gt, stream);
+}
+
+}  // namespace bpe

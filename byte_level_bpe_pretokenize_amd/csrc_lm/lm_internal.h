@@ -137,4 +137,125 @@ void block_divisor(int32_t bs, uint32_t *magic, int32_t *shift);
 
 hipError_t launch_blocks(const BlockArgs &a, hipStream_t stream);
 
+// ---- a cache of few bits -----------------------------------------------------------
+constexpr int kCacheThreads = 256;
+constexpr int kCacheVec = 8;       // elements per lane
+constexpr int kCacheTokens = 64;   // tokens per workgroup, at most
+constexpr int kCacheMinGroup = 16, kCacheMaxGroup = 64 * kCacheVec;  // a wave's lanes at most
+
+// x / d for 0 <= x < 2^31 by a multiplication (block_divisor).
+struct Divisor {
+  uint32_t magic;
+  int32_t shift, d;
+};
+Divisor divisor(int32_t d);
+
+struct CacheArgs {
+  bpe_cache c;
+  int32_t row_bytes;      // codes of one head
+  int32_t groups;         // of one head
+  int32_t group_log2;
+  int64_t n;              // tokens
+  int64_t t_stride, h_stride;
+  int32_t *status;
+  // a token's lanes, kCacheVec elements each: lanes per head and per token (a
+  // write has whole groups of lanes per group of elements)
+  Divisor per_head, per_token;
+  int32_t tokens;         // per workgroup
+  // write
+  const void *x;
+  const int64_t *slots;
+  // read
+  void *out;
+  const int32_t *table, *start;
+  const int64_t *off;
+  int64_t R, width, stride;
+  Divisor bs;
+};
+
+int32_t cache_groups(const bpe_cache &c);
+int32_t cache_row_bytes(const bpe_cache &c);
+bool cache_ok(const bpe_cache &c);
+bool cache_tokens_ok(const bpe_cache &c, int64_t n, int64_t token_stride, int64_t head_stride);
+void cache_shape(CacheArgs *a, bool write);
+inline int64_t cache_workgroups(const CacheArgs &a) { return (a.n + a.tokens - 1) / a.tokens; }
+
+#if defined(__HIPCC__)
+#define BPE_HD __host__ __device__ __forceinline__
+#else
+#define BPE_HD inline
+#endif
+
+// The slot of position p of a request whose blocks are row[0 .. width), or -1
+// where it is read as zeros; *status gets why.
+BPE_HD int64_t cache_slot(const int32_t *row, int64_t width, int32_t bs, int64_t n_slots,
+                          int64_t p, int32_t block, uint32_t *status) {
+  if (block >= width) {
+    *status |= BPE_STATUS_TABLE_FULL;
+    return -1;
+  }
+  const int32_t entry = row[block];
+  if (entry < 0) return -1;
+  const int64_t slot = (int64_t)entry * bs + (p - (int64_t)block * bs);
+  if (slot >= n_slots) {
+    *status |= BPE_STATUS_BAD_SLOT;
+    return -1;
+  }
+  return slot;
+}
+
+// The first request in [lo, hi) that ends behind token t, or hi.  In range also
+// for offsets that do not increase.  (Growing steps from lo on would take fewer
+// loads, but hipcc 7.2 miscompiles their 64-bit minimum: the select that it makes
+// for it takes the carry of the sum before it.)
+BPE_HD int64_t cache_request(const int64_t *off, int64_t lo, int64_t hi, int64_t t) {
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (off[mid + 1] <= t) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+hipError_t launch_cache_write(const CacheArgs &a, int xt, hipStream_t stream);
+hipError_t launch_cache_read(const CacheArgs &a, int ot, hipStream_t stream);
+
+// ---- drafted tokens -----------------------------------------------------------------
+constexpr int kVerifyThreads = 1024;  // a workgroup per request
+
+struct VerifyArgs {
+  const void *target, *draft;
+  int64_t n_rows, vocab, t_stride, d_stride;
+  const int32_t *ids;
+  const int64_t *off;
+  int64_t R;
+  const float *accept, *sample;
+  int32_t *tokens, *counts, *status;
+};
+
+hipError_t launch_verify(const VerifyArgs &a, int type, hipStream_t stream);
+
+// ---- distillation -------------------------------------------------------------------
+constexpr int kDistillSlab = 8192;    // logits per workgroup of the gradient
+constexpr int kDistillThreads = 256;
+constexpr int kDistillWide = 1024;    // threads of the loss's widest workgroup
+
+struct DistillArgs {
+  const void *student, *teacher;
+  int64_t rows, vocab, s_stride, t_stride;
+  const int32_t *ids;
+  int64_t i_stride;
+  int32_t top;
+  float temperature;
+  float *losses, *stats;       // the loss's
+  const float *in_stats, *dloss;  // the gradient's
+  void *grad;
+  int64_t g_stride;
+  int32_t *status;
+};
+
+bool distill_grad_fits(int64_t n_rows, int64_t vocab);
+hipError_t launch_distill(const DistillArgs &a, int st, int tt, hipStream_t stream);
+hipError_t launch_distill_grad(const DistillArgs &a, int st, int tt, int gt, hipStream_t stream);
+
 }  // namespace bpe

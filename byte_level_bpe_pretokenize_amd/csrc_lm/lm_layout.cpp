@@ -103,4 +103,63 @@ void block_divisor(int32_t bs, uint32_t *magic, int32_t *shift) {
   *shift = s - 1;  // of the product's upper half
 }
 
+Divisor divisor(int32_t d) {
+  Divisor r = {};
+  r.d = d;
+  if (d > 1) block_divisor(d, &r.magic, &r.shift);
+  return r;
+}
+
+int32_t cache_groups(const bpe_cache &c) { return (c.dim + c.group - 1) / c.group; }
+
+int32_t cache_row_bytes(const bpe_cache &c) {
+  return c.format == BPE_UINT4 ? (c.dim + 1) / 2 : c.dim;
+}
+
+bool cache_ok(const bpe_cache &c) {
+  if ((c.format != BPE_E4M3 && c.format != BPE_INT8 && c.format != BPE_UINT4) || c.heads < 1 ||
+      c.heads > BPE_MAX_HEADS || c.dim < 1 || c.dim > BPE_MAX_DIM || c.group < kCacheMinGroup ||
+      c.group > kCacheMaxGroup || (c.group & (c.group - 1)) || c.n_slots < 0 ||
+      c.n_slots > (int64_t)1 << 40)
+    return false;
+  const int64_t most = (int64_t)1 << 32;
+  const int64_t scales = (int64_t)c.heads * cache_groups(c) * (c.format == BPE_UINT4 ? 2 : 1);
+  // (2^40 slots of 2^22 bytes are addressed in 64 bits)
+  return c.codes_stride >= (int64_t)c.heads * cache_row_bytes(c) && c.codes_stride <= most >> 10 &&
+         c.scales_stride >= scales && c.scales_stride <= most >> 12 &&
+         (c.n_slots == 0 || (c.codes && c.scales));
+}
+
+// Strides of tokens and heads: token by token or head by head, without overlap.
+bool cache_tokens_ok(const bpe_cache &c, int64_t n, int64_t token_stride, int64_t head_stride) {
+  const int64_t most = (int64_t)1 << 32;
+  if (n < 0 || n > BPE_MAX_IDS || n * c.heads >= most) return false;
+  const bool many = n > 1, heads = c.heads > 1;
+  if ((many && (token_stride < c.dim || token_stride > most)) ||
+      (heads && (head_stride < c.dim || head_stride > most)))
+    return false;
+  return !many || !heads || token_stride >= (c.heads - 1) * head_stride + c.dim ||
+         head_stride >= (n - 1) * token_stride + c.dim;
+}
+
+// A token's lanes, and tokens per workgroup: four vectors per thread where
+// there are that many.
+void cache_shape(CacheArgs *a, bool write) {
+  a->row_bytes = cache_row_bytes(a->c);
+  a->groups = cache_groups(a->c);
+  a->group_log2 = 0;
+  while (1 << a->group_log2 < a->c.group) ++a->group_log2;
+  const int32_t per_head = write ? a->groups * (a->c.group / kCacheVec)
+                                 : (a->c.dim + kCacheVec - 1) / kCacheVec;
+  a->per_head = divisor(per_head);
+  a->per_token = divisor(per_head * a->c.heads);
+  const int32_t tokens = 4 * kCacheThreads / (per_head * a->c.heads);
+  a->tokens = tokens < 1 ? 1 : tokens > kCacheTokens ? kCacheTokens : tokens;
+}
+
+// Whether the gradient is one launch.
+bool distill_grad_fits(int64_t n_rows, int64_t vocab) {
+  return launch_fits((vocab + kDistillSlab - 1) / kDistillSlab * n_rows, kDistillThreads);
+}
+
 }  // namespace bpe

@@ -5,7 +5,12 @@ in include/bpe_lm.h (argument marshalling only).
 IDs that ``Model.encode_batch`` gives, scaled, and the table's gradient.
 ``process_logits``: penalties for repeated tokens, biases and grammar masks on
 the logits of the next token.  ``block_tables``: block tables, slots and
-positions of a paged cache from the requests' lengths.
+positions of a paged cache from the requests' lengths.  ``cache_write`` /
+``cache_read``: a paged cache held in 8 or 4 bits, written by those slots and
+read by those tables.  ``verify_drafts``: which drafted tokens stand against the
+target's probabilities, and the token drawn after them.  ``distill`` /
+``distill_grad`` / ``distillation``: loss on a teacher's top logits, and its
+gradient.
 
 Every call takes ``status``, an int32 device tensor of one element that the
 caller has cleared: the call ORs _lib.STATUS_* bits into it and does not
@@ -13,9 +18,9 @@ synchronize.  Without one the call makes its own, waits for it, and raises
 where a bit is set (so a call that is captured into a graph needs one).  Work
 goes to ``stream``, or the current stream.
 
-Only ``embedding`` takes part in autograd.  The other calls raise where grad
-mode is on and a matrix or vector given to them requires a gradient, which
-they would drop; what they write in place counts as modified.
+Only ``embedding`` and ``distillation`` take part in autograd.  The other calls
+raise where grad mode is on and a matrix or vector given to them requires a
+gradient, which they would drop; what they write in place counts as modified.
 """
 from __future__ import annotations
 
@@ -27,6 +32,8 @@ from . import _lib
 from .api import BPEError
 
 _TYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
+# what a cache's codes are kept as: uint8 holds two of 4 bits
+_FORMATS = {torch.float8_e4m3fn: _lib.E4M3, torch.int8: _lib.INT8, torch.uint8: _lib.UINT4}
 
 
 # the current stream's handle by device index; a stream object costs 20 times
@@ -444,3 +451,306 @@ def block_tables(new_off: torch.Tensor, n_new: int, cached: torch.Tensor,
     _modified(filled)
     _end("bpe_block_tables", rc, st if status is None else None)
     return slots, positions, lengths, used
+
+
+def empty_cache(n_slots: int, heads: int, dim: int, dtype: torch.dtype = torch.float8_e4m3fn,
+                group: int | None = None, device="cuda"):
+    """A cache of n_slots tokens for cache_write and cache_read, not cleared:
+    (codes, scales, group).  dtype: float8_e4m3fn, int8, or uint8 for 4 bits (two
+    to a byte).  group: elements per scale, a power of two from 16 to 512 (by
+    default the first that holds a head, 512 at most)."""
+    if dtype not in _FORMATS:
+        raise TypeError(f"dtype: float8_e4m3fn, int8 or uint8 expected, got {dtype}")
+    if group is None:
+        group = min(512, max(16, 1 << (dim - 1).bit_length()))
+    four = dtype == torch.uint8
+    G = -(-dim // group)
+    codes = torch.empty((n_slots, heads, (dim + 1) // 2 if four else dim), dtype=torch.uint8, device=device)
+    scales = torch.empty((n_slots, heads, G, 2) if four else (n_slots, heads, G), device=device)
+    return codes.view(dtype), scales, group
+
+
+def _cache(codes: torch.Tensor, scales: torch.Tensor, group: int, heads: int, dim: int):
+    """bpe_cache of a cache's tensors."""
+    form = _FORMATS.get(codes.dtype)
+    if form is None:
+        raise TypeError(f"codes: float8_e4m3fn, int8 or uint8 expected, got {codes.dtype}")
+    if scales.dtype is not torch.float32:
+        raise TypeError(f"scales: torch.float32 expected, got {scales.dtype}")
+    group = _int32(group, 1, "group")
+    n = codes.shape[0]
+    row = (heads, dim if form != _lib.UINT4 else (dim + 1) // 2)
+    if tuple(codes.shape[1:]) != row:
+        raise ValueError(f"codes: (slots, {row[0]}, {row[1]}) expected, got {tuple(codes.shape)}")
+    G = -(-dim // group)
+    srow = (heads, G) if form != _lib.UINT4 else (heads, G, 2)
+    if scales.shape[0] != n or tuple(scales.shape[1:]) != srow:
+        raise ValueError(f"scales: {(n, *srow)} expected, got {tuple(scales.shape)}")
+    cs, ss = row[0] * row[1], heads * G * (2 if form == _lib.UINT4 else 1)
+    if n:
+        if not codes[0].is_contiguous() or not scales[0].is_contiguous():
+            raise ValueError("codes, scales: expected slots of consecutive elements")
+        if n > 1:
+            if codes.stride(0) < cs or scales.stride(0) < ss:
+                raise ValueError("codes, scales: expected slots that do not overlap")
+            cs, ss = codes.stride(0), scales.stride(0)
+    return _lib.Cache(codes.data_ptr() if n else None, scales.data_ptr() if n else None, n, cs, ss,
+                      heads, dim, group, form)
+
+
+def _tokens(t: torch.Tensor, what: str):
+    """(token stride, head stride) of (n, heads, dim) whose heads are consecutive
+    elements; 0 where there is one token or one head."""
+    n, H, D = t.shape
+    if D > 1 and t.stride(2) != 1:
+        raise ValueError(f"{what}: expected heads of consecutive elements")
+    ts, hs = t.stride(0) if n > 1 else 0, t.stride(1) if H > 1 else 0
+    if (n > 1 and ts < D) or (H > 1 and hs < D) or \
+            (n > 1 and H > 1 and ts < (H - 1) * hs + D and hs < (n - 1) * ts + D):
+        raise ValueError(f"{what}: expected heads that do not overlap")
+    return ts, hs
+
+
+def cache_write(x: torch.Tensor, slots: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                group: int, *, status: torch.Tensor | None = None, stream=None) -> None:
+    """bpe_cache_write: quantises the tokens ``x`` (n, heads, dim) into ``slots``
+    (int64, as block_tables gives them; -1: nowhere) of a cache, in place.
+
+    codes (S, heads, dim) of float8_e4m3fn or int8, or (S, heads, ceil(dim / 2))
+    uint8 for 4 bits; scales float32 (S, heads, ceil(dim / group)), with a last
+    dimension of 2 for 4 bits (scale, lowest value).  Keys and values side by side
+    are one call of twice the heads.  Slots must differ."""
+    if stream is not None:
+        return _on(stream, cache_write, (x, slots, codes, scales, status), x, slots, codes, scales,
+                   group, status=status)
+    _no_gradient("cache_write", "call it ", (x, scales))
+    xt = _type(x.dtype, "x")
+    if x.dim() != 3:
+        raise ValueError(f"x: (n, heads, dim) expected, got {x.dim()} dimensions")
+    n, H, D = x.shape
+    ts, hs = _tokens(x, "x")
+    sp = _list(slots, torch.int64, n, "slots")
+    c = _cache(codes, scales, group, H, D)
+    dev = _device("cache_write", (x, slots, codes, scales, status))
+    st = _status(status, dev)
+    rc = _lib.load().bpe_cache_write(C.byref(c), x.data_ptr(), xt, n, ts, hs, sp, st.data_ptr(), _stream(dev))
+    _modified([codes, scales])
+    _end("bpe_cache_write", rc, st if status is None else None)
+
+
+def cache_read(codes: torch.Tensor, scales: torch.Tensor, group: int, table: torch.Tensor,
+               block_size: int, off: torch.Tensor, n: int, *, dim: int | None = None,
+               start: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               out_dtype: torch.dtype | None = None, status: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """bpe_cache_read: the values of the requests' tokens, packed: (n, heads, dim)
+    of ``out_dtype`` (bfloat16 by default), or ``out``, filled.
+
+    codes, scales, group: a cache as cache_write takes it; table int32 (R, W), as
+    block_tables keeps it, of blocks of ``block_size``; off int64 (R + 1): the
+    requests' places in the packed tokens, n in all; start int32 (R): the position
+    of each request's first one (0 by default).  ``dim``: a head's elements
+    (needed for an odd head of 4 bits)."""
+    if stream is not None:
+        kw = dict(start=start, out=out, status=status)
+        return _on(stream, cache_read, (codes, scales, table, off, *kw.values()), codes, scales, group,
+                   table, block_size, off, n, dim=dim, out_dtype=out_dtype, **kw)
+    _no_gradient("cache_read", "call it ", (scales, out))
+    if codes.dim() != 3:
+        raise ValueError(f"codes: 3 dimensions expected, got {codes.dim()}")
+    H = codes.shape[1]
+    if dim is None:
+        dim = out.shape[2] if out is not None and out.dim() == 3 else \
+            codes.shape[2] * (2 if codes.dtype == torch.uint8 else 1)
+    c = _cache(codes, scales, group, H, dim)
+    if table.dtype is not torch.int32:
+        raise TypeError(f"table: torch.int32 expected, got {table.dtype}")
+    tstr = _rows(table, "table")
+    R, W = table.shape
+    op = _list(off, torch.int64, R + 1, "off")
+    fp = None if start is None else _list(start, torch.int32, R, "start")
+    block_size = _int32(block_size, 1, "block_size")
+    if n < 0:
+        raise ValueError(f"n: {n} is out of range")
+    if out is None:
+        dt = torch.bfloat16 if out_dtype is None else out_dtype
+        ot, ts, hs = _type(dt, "out_dtype"), H * dim, dim
+    else:
+        ot = _type(out.dtype, "out")
+        if tuple(out.shape) != (n, H, dim) or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out: ({n}, {H}, {dim}) of out_dtype expected, got {tuple(out.shape)}")
+        ts, hs = _tokens(out, "out")
+    dev = _device("cache_read", (codes, scales, table, off, start, out, status))
+    st = _status(status, dev)
+    res = torch.empty((n, H, dim), dtype=dt, device=codes.device) if out is None else out
+    rc = _lib.load().bpe_cache_read(C.byref(c), table.data_ptr(), R, W, tstr, block_size, op, fp, n,
+                                    res.data_ptr(), ot, ts, hs, st.data_ptr(), _stream(dev))
+    if out is not None:
+        _modified(out)
+    _end("bpe_cache_read", rc, st if status is None else None)
+    return res
+
+
+def verify_drafts(target: torch.Tensor, draft_ids: torch.Tensor, row_off: torch.Tensor,
+                  accept: torch.Tensor, sample: torch.Tensor, *, draft: torch.Tensor | None = None,
+                  tokens: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                  status: torch.Tensor | None = None, stream=None):
+    """bpe_verify_drafts: (tokens int32 (N), counts int32 (R)), new or the tensors
+    given: each request's drafted tokens that stand and the one drawn after them,
+    then -1, in its rows; and how many it got.
+
+    target (N, V): the target's probabilities; row_off int64 (R + 1): the requests'
+    rows, one more than their drafts.  draft_ids int32 (N): the token that a row
+    verifies (its request's last row: anything); draft (N, V): the probabilities it
+    was drawn from, None where the drafts were certain.  accept float32 (N), sample
+    float32 (R): uniform in [0, 1)."""
+    if stream is not None:
+        kw = dict(draft=draft, tokens=tokens, counts=counts, status=status)
+        return _on(stream, verify_drafts, (target, draft_ids, row_off, accept, sample, *kw.values()),
+                   target, draft_ids, row_off, accept, sample, **kw)
+    _no_gradient("verify_drafts", "call it ", (target, draft, accept, sample))
+    pt, ps = _type(target.dtype, "target"), _rows(target, "target")
+    N, V = target.shape
+    R = row_off.numel() - 1
+    qp, qs = None, 0
+    if draft is not None:
+        if draft.dtype is not target.dtype:
+            raise TypeError(f"draft: {target.dtype} expected, got {draft.dtype}")
+        qs = _rows(draft, "draft")
+        if draft.shape != target.shape:
+            raise ValueError(f"draft: {tuple(target.shape)} expected, got {tuple(draft.shape)}")
+        qp = draft.data_ptr()
+    ip = _list(draft_ids, torch.int32, N, "draft_ids")
+    op = _list(row_off, torch.int64, -1, "row_off")
+    if R < 0:
+        raise ValueError("row_off: one entry more than requests expected, got none")
+    ap = _list(accept, torch.float32, N, "accept")
+    sp = _list(sample, torch.float32, R, "sample")
+    if tokens is not None:
+        _list(tokens, torch.int32, N, "tokens")
+    if counts is not None:
+        _list(counts, torch.int32, R, "counts")
+    dev = _device("verify_drafts", (target, draft, draft_ids, row_off, accept, sample, tokens, counts, status))
+    st = _status(status, dev)
+    filled = [t for t in (tokens, counts) if t is not None]
+    if tokens is None:
+        tokens = draft_ids.new_empty(N)
+    if counts is None:
+        counts = draft_ids.new_empty(R)
+    rc = _lib.load().bpe_verify_drafts(target.data_ptr(), pt, N, V, ps, qp, qs, ip, op, R, ap, sp,
+                                       tokens.data_ptr(), counts.data_ptr(), st.data_ptr(), _stream(dev))
+    if filled:
+        _modified(filled)
+    _end("bpe_verify_drafts", rc, st if status is None else None)
+    return tokens, counts
+
+
+def _teacher(student, ids, teacher):
+    """What a student's and a teacher's rows are passed as."""
+    zt, zs = _type(student.dtype, "student"), _rows(student, "student")
+    tt, ts = _type(teacher.dtype, "teacher"), _rows(teacher, "teacher")
+    if ids.dtype is not torch.int32:
+        raise TypeError(f"ids: torch.int32 expected, got {ids.dtype}")
+    is_ = _rows(ids, "ids")
+    N, V = student.shape
+    if ids.shape != teacher.shape or ids.shape[0] != N:
+        raise ValueError(f"ids, teacher: {N} rows of the same width expected, got {tuple(ids.shape)} "
+                         f"and {tuple(teacher.shape)}")
+    return (student.data_ptr(), zt, N, V, zs, ids.data_ptr(), is_, teacher.data_ptr(), tt, ts, ids.shape[1])
+
+
+def distill(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, temperature: float = 1.0,
+            *, losses: torch.Tensor | None = None, stats: torch.Tensor | None = None,
+            status: torch.Tensor | None = None, stream=None):
+    """bpe_distill: (losses float32 (N), stats float32 (N, 4)), new or the tensors
+    given: temperature^2 times the divergence of the student's distribution from
+    the teacher's over its listed tokens, and what distill_grad needs.
+
+    student (N, V): logits; ids int32 (N, K): the teacher's top tokens, -1 for
+    none; teacher (N, K): their logits."""
+    if stream is not None:
+        kw = dict(losses=losses, stats=stats, status=status)
+        return _on(stream, distill, (student, ids, teacher, *kw.values()), student, ids, teacher,
+                   temperature, **kw)
+    _no_gradient("distill", "call distillation instead, or distill ", (student, teacher))
+    a = _teacher(student, ids, teacher)
+    N = a[2]
+    if losses is not None:
+        _list(losses, torch.float32, N, "losses")
+    if stats is not None:
+        _list(stats, torch.float32, N * 4, "stats")
+    dev = _device("distill", (student, ids, teacher, losses, stats, status))
+    st = _status(status, dev)
+    filled = [t for t in (losses, stats) if t is not None]
+    if losses is None:
+        losses = student.new_empty(N, dtype=torch.float32)
+    if stats is None:
+        stats = student.new_empty((N, 4), dtype=torch.float32)
+    rc = _lib.load().bpe_distill(*a, temperature, losses.data_ptr(), stats.data_ptr(), st.data_ptr(),
+                                 _stream(dev))
+    if filled:
+        _modified(filled)
+    _end("bpe_distill", rc, st if status is None else None)
+    return losses, stats
+
+
+def distill_grad(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, stats: torch.Tensor,
+                 dloss: torch.Tensor, temperature: float = 1.0, *, out: torch.Tensor | None = None,
+                 out_dtype: torch.dtype | None = None, status: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """bpe_distill_grad: the gradient of ``distill``'s losses, weighted by ``dloss``
+    float32 (N), with respect to the student's logits: (N, V) of ``out_dtype`` (the
+    student's by default), or ``out``, which may be the student itself, filled.
+    stats: what distill gave for the same inputs."""
+    if stream is not None:
+        kw = dict(out=out, status=status)
+        return _on(stream, distill_grad, (student, ids, teacher, stats, dloss, *kw.values()), student,
+                   ids, teacher, stats, dloss, temperature, out_dtype=out_dtype, **kw)
+    _no_gradient("distill_grad", "call it ", (student, teacher, stats, dloss, out))
+    a = _teacher(student, ids, teacher)
+    N, V = a[2:4]
+    sp = _list(stats, torch.float32, N * 4, "stats")
+    dp = _list(dloss, torch.float32, N, "dloss")
+    if out is None:
+        dt = student.dtype if out_dtype is None else out_dtype
+        ot, os_ = _type(dt, "out_dtype"), V
+    else:
+        ot, os_ = _type(out.dtype, "out"), _rows(out, "out")
+        if out.shape != student.shape or out_dtype not in (None, out.dtype):
+            raise ValueError(f"out: {tuple(student.shape)} of out_dtype expected, got {tuple(out.shape)}")
+    dev = _device("distill_grad", (student, ids, teacher, stats, dloss, out, status))
+    st = _status(status, dev)
+    res = student.new_empty((N, V), dtype=dt) if out is None else out
+    rc = _lib.load().bpe_distill_grad(*a, sp, dp, temperature, res.data_ptr(), ot, os_, st.data_ptr(),
+                                      _stream(dev))
+    if out is not None:
+        _modified(out)
+    _end("bpe_distill_grad", rc, st if status is None else None)
+    return res
+
+
+class _Distillation(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, student, ids, teacher, temperature, status):
+        losses, stats = distill(student, ids, teacher, temperature, status=status)
+        ctx.save_for_backward(student, ids, teacher, stats)
+        ctx.distill = (temperature, status)
+        return losses
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        if not ctx.needs_input_grad[0]:
+            return (None,) * 5
+        student, ids, teacher, stats = ctx.saved_tensors
+        temperature, status = ctx.distill
+        g = distill_grad(student, ids, teacher, stats, dloss.contiguous(), temperature, status=status)
+        return g, None, None, None, None
+
+
+def distillation(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                 temperature: float = 1.0, *, status: torch.Tensor | None = None) -> torch.Tensor:
+    """``distill``'s losses with ``distill_grad`` as their gradient for autograd, on
+    the current stream.  The teacher gets no gradient."""
+    _no_gradient("distillation's teacher", "call it ", (teacher,))
+    return _Distillation.apply(student, ids, teacher, temperature, status)
