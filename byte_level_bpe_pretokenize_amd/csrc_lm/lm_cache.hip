@@ -36,127 +36,201 @@ __device__ __forceinline__ void store_some(T *p, const Vec<T, E> &x, int m) {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
-// The codes of E numbers that are within the format's range, as bytes.
+// Bytes in device memory, at any address.
+typedef uint32_t b4 __attribute__((aligned(1)));
+typedef uint32_t b8 __attribute__((ext_vector_type(2), aligned(1)));
+
+// The largest of `lanes` (a power of two, the same in every lane) neighbouring
+// lanes' values, in each of them; every lane active.  Lanes 1 and 2 away by quad,
+// then, since quads and halves agree within, by mirroring 8 and 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ float other(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lanes_max(float x, int lanes) {
+  x = fmaxf(x, other<0xB1>(x));
+  if (lanes > 2) x = fmaxf(x, other<0x4E>(x));
+  if (lanes > 4) x = fmaxf(x, other<0x141>(x));
+  if (lanes > 8) x = fmaxf(x, other<0x140>(x));
+  if (lanes > 16) x = fmaxf(x, __shfl_xor(x, 16, 64));
+  if (lanes > 32) x = fmaxf(x, __shfl_xor(x, 32, 64));
+  return x;
+}
+
+// The codes of E numbers within the format's range (up to float32's rounding of
+// its ends, which rounds back to them), in the first bytes of w.
 template <int F>
-__device__ __forceinline__ Vec<uint8_t, E> encode(const float *y) {
-  Vec<uint8_t, E> r;
+__device__ __forceinline__ void encode(const float *y, uint32_t *w) {
   if (F == BPE_E4M3) {
-    int32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
       w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w[i], true);
     }
-    __builtin_memcpy(&r, w, 8);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) r.v[e] = (uint8_t)(int32_t)rintf(y[e]);
+    return;
   }
-  return r;
+  // adding 1.5 * 2^23 rounds to a whole number, to nearest even, in the low bits
+  uint32_t b[E];
+  {
+#pragma clang fp contract(off)
+#pragma unroll
+    for (int e = 0; e < E; ++e) b[e] = __float_as_uint(y[e] + 12582912.f);
+  }
+  if (F == BPE_INT8) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __builtin_amdgcn_perm(b[4 * i + 1], b[4 * i], 0x0c0c0400);
+      const uint32_t hi = __builtin_amdgcn_perm(b[4 * i + 3], b[4 * i + 2], 0x0c0c0400);
+      w[i] = __builtin_amdgcn_perm(hi, lo, 0x05040100);
+    }
+  } else {
+    w[0] = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) w[0] |= (b[e] & 15u) << 4 * e;
+  }
+}
+
+// The scale and lowest value of a group that has infinities, NaN or magnitudes past
+// 2^126, and its elements as they are to be held.
+template <int F>
+__device__ __forceinline__ void rare(float *y, int m, int lanes, float *scale, float *low) {
+  float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if (!finite(y[e])) continue;
+    if (F == BPE_UINT4) y[e] = fminf(fmaxf(y[e], -0x1p126f), 0x1p126f);
+    if (e < m) {
+      lo = fminf(lo, F == BPE_UINT4 ? y[e] : -fabsf(y[e]));
+      hi = fmaxf(hi, F == BPE_UINT4 ? y[e] : fabsf(y[e]));
+    }
+  }
+  lo = -lanes_max(-lo, lanes);
+  hi = lanes_max(hi, lanes);
+  const bool some = lo <= hi;
+  *low = some && F == BPE_UINT4 ? lo : 0.f;
+  *scale = !some ? 0.f
+           : F == BPE_UINT4 ? (hi - lo) * (1.0f / 15.0f)
+                            : hi * (F == BPE_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f);
 }
 
 // A group's elements are held by group / E neighbouring lanes.  Their range by
 // exchange between these lanes, the codes by one multiplication each (the
 // inverse is rounded once per group).  A workgroup has whole tokens.
-template <typename T, int F>
+template <typename T, int F, bool WHOLE>
 __global__ void __launch_bounds__(CT) k_cache_write(CacheArgs a) {
-  const int lanes = 1 << (a.group_log2 - 3);  // of a group
   static_assert(E == 8, "group / 8 lanes");
+  constexpr int U = 4;
+  const int lanes = 1 << (a.group_log2 - 3);  // of a group
+  const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
   const int count = (int)min<int64_t>(a.tokens, a.n - t0) * a.per_token.d;
   uint32_t status = 0;
-  for (int i = threadIdx.x; i - (int)threadIdx.x < count; i += CT) {
-    // (lanes past the end take part in the exchange)
-    const bool in = i < count;
-    const int j = in ? i : 0;
-    const int token = divide(a.per_token, j);
-    const int k = j - token * a.per_token.d;  // lane of the token
-    const int head = divide(a.per_head, k);
-    const int l = k - head * a.per_head.d;    // lane of the head
-    const int group = l >> (a.group_log2 - 3);
-    const int c = l * E;                      // first element
-    const int m = in ? a.c.dim - c : 0;       // elements there
-    const T *x = (const T *)a.x + (t0 + token) * a.t_stride + head * a.h_stride + c;
-    const int64_t slot = in ? a.slots[t0 + token] : -1;
-    Vec<T, E> v = {};
-    if (m > 0) v = load_some(x, m);
-    float y[E];
-    bool all_finite = true;
+  for (int base = 0; base < count; base += CT * U) {
+    Vec<T, E> v[U];
+    int64_t slot[U];
+    int head[U], l[U], m[U];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      y[e] = (float)v.v[e];
-      all_finite &= finite(y[e]);
+    for (int u = 0; u < U; ++u) {
+      // (lanes past the end take part in the exchange, with the last group's values)
+      const int i = base + u * CT + tid;
+      const int j = i < count ? i : count - lanes + (i & (lanes - 1));
+      const int token = divide(a.per_token, j);
+      const int k = j - token * a.per_token.d;  // lane of the token
+      head[u] = divide(a.per_head, k);
+      l[u] = k - head[u] * a.per_head.d;        // lane of the head
+      m[u] = a.c.dim - l[u] * E;                // elements there
+      slot[u] = a.slots[t0 + token];
+      const T *x = (const T *)a.x + (t0 + token) * a.t_stride + head[u] * a.h_stride + l[u] * E;
+      // (a head's last group may end before its last lanes)
+      if (m[u] >= E) v[u] = load_vec<T, E>(x);
+      else if (WHOLE || m[u] <= 0) v[u] = Vec<T, E>{};
+      else v[u] = load_some(x, m[u]);
+      if (i >= count) m[u] = 0;
     }
-    if (!all_finite && slot >= 0) status |= BPE_STATUS_NOT_FINITE;
-    float scale, low = 0.f;
-    if (F == BPE_UINT4) {
-      float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float y[E], most = 0.f, zero = 0.f;
+      // (a NaN drops out of the maximum; it and infinities show in the sum)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        if (finite(y[e])) y[e] = fminf(fmaxf(y[e], -0x1p126f), 0x1p126f);
-        if (e < m && finite(y[e])) {
-          lo = fminf(lo, y[e]);
-          hi = fmaxf(hi, y[e]);
+        y[e] = (float)v[u].v[e];
+        most = fmaxf(most, fabsf(y[e]));
+        zero = fmaf(y[e], 0.f, zero);
+      }
+      const bool odd = zero != 0.f || (F == BPE_UINT4 && most > 0x1p126f);
+      float scale, low = 0.f;
+      if (F == BPE_UINT4) {
+        float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          lo = fminf(lo, WHOLE || e < m[u] ? y[e] : INFINITY);
+          hi = fmaxf(hi, WHOLE || e < m[u] ? y[e] : -INFINITY);
         }
+        if (WHOLE && m[u] <= 0) {  // (the values there are no element's)
+          lo = INFINITY;
+          hi = -INFINITY;
+        }
+        low = -lanes_max(-lo, lanes);
+        scale = (lanes_max(hi, lanes) - low) * (1.0f / 15.0f);
+      } else {
+        scale = lanes_max(most, lanes) * (F == BPE_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f);
       }
-      for (int d = 1; d < lanes; d <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, d, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, d, 64));
+      const bool any_odd = __any(odd);
+      if (any_odd) {
+        if (zero != 0.f && m[u] > 0 && slot[u] >= 0) status |= BPE_STATUS_NOT_FINITE;
+        rare<F>(y, m[u], lanes, &scale, &low);
       }
-      const bool some = lo <= hi;
-      low = some ? lo : 0.f;
-      scale = some ? (hi - lo) * (1.0f / 15.0f) : 0.f;
-    } else {
-      float most = 0.f;
+      if (scale < 0x1p-120f) scale = 0.f;
+      const float inverse = scale > 0.f ? 1.0f / scale : 0.f;
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (finite(y[e])) most = fmaxf(most, fabsf(y[e]));
-      for (int d = 1; d < lanes; d <<= 1) most = fmaxf(most, __shfl_xor(most, d, 64));
-      scale = most * (F == BPE_E4M3 ? 1.0f / 448.0f : 1.0f / 127.0f);
-    }
-    if (scale < 0x1p-120f) scale = 0.f;
-    const float inverse = scale > 0.f ? 1.0f / scale : 0.f;
-    constexpr float top = F == BPE_E4M3 ? 448.f : F == BPE_INT8 ? 127.f : 15.f;
-    constexpr float bottom = F == BPE_UINT4 ? 0.f : -top;
+      for (int e = 0; e < E; ++e) y[e] = (F == BPE_UINT4 ? y[e] - low : y[e]) * inverse;
+      if (any_odd) {
+        constexpr float top = F == BPE_E4M3 ? 448.f : F == BPE_INT8 ? 127.f : 15.f;
+        constexpr float bottom = F == BPE_UINT4 ? 0.f : -top;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      y[e] = (F == BPE_UINT4 ? y[e] - low : y[e]) * inverse;
-      // (a NaN is one, or an infinity in a group of scale 0)
-      y[e] = y[e] == y[e] ? fminf(fmaxf(y[e], bottom), top) : 0.f;
-    }
-    if (slot < -1 || slot >= a.c.n_slots) status |= BPE_STATUS_BAD_SLOT;
-    if (m <= 0 || slot < 0 || slot >= a.c.n_slots) continue;
-    const Vec<uint8_t, E> codes = encode<F>(y);
-    uint8_t *q = (uint8_t *)a.c.codes + slot * a.c.codes_stride + (int64_t)head * a.row_bytes;
-    if (F == BPE_UINT4) {
-      Vec<uint8_t, E / 2> h;
+        for (int e = 0; e < E; ++e)  // (a NaN is one, or an infinity in a group of scale 0)
+          y[e] = y[e] == y[e] ? fminf(fmaxf(y[e], bottom), top) : 0.f;
+      }
+      if (slot[u] < -1 || slot[u] >= a.c.n_slots) status |= BPE_STATUS_BAD_SLOT;
+      if (m[u] <= 0 || slot[u] < 0 || slot[u] >= a.c.n_slots) continue;
+      uint32_t w[2];
+      encode<F>(y, w);
+      uint8_t *q = (uint8_t *)a.c.codes + slot[u] * a.c.codes_stride + head[u] * a.row_bytes +
+                   l[u] * (F == BPE_UINT4 ? E / 2 : E);
+      if (WHOLE || m[u] >= E) {
+        if (F == BPE_UINT4) *(b4 *)q = w[0];
+        else *(b8 *)q = b8{w[0], w[1]};
+      } else if (F == BPE_UINT4) {
+        w[0] &= (1u << 4 * m[u]) - 1u;
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e)
-        h.v[e] = (uint8_t)(codes.v[2 * e] | (2 * e + 1 < m ? codes.v[2 * e + 1] << 4 : 0));
-      q += c / 2;
+        for (int e = 0; e < E / 2; ++e)
+          if (2 * e < m[u]) q[e] = (uint8_t)(w[0] >> 8 * e);
+      } else {
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e)
-        if (2 * e < m) q[e] = h.v[e];
-    } else {
-      q += c;
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (e < m) q[e] = codes.v[e];
-    }
-    if ((l & (lanes - 1)) == 0) {
-      float *s = a.c.scales + slot * a.c.scales_stride +
-                 ((int64_t)head * a.groups + group) * (F == BPE_UINT4 ? 2 : 1);
-      s[0] = scale;
-      if (F == BPE_UINT4) s[1] = low;
+        for (int e = 0; e < E; ++e)
+          if (e < m[u]) q[e] = (uint8_t)(w[e >> 2] >> 8 * (e & 3));
+      }
+      if ((l[u] & (lanes - 1)) == 0) {
+        float *s = a.c.scales + slot[u] * a.c.scales_stride +
+                   (head[u] * a.groups + (l[u] >> (a.group_log2 - 3))) * (F == BPE_UINT4 ? 2 : 1);
+        s[0] = scale;
+        if (F == BPE_UINT4) s[1] = low;
+      }
     }
   }
   if (status) atomicOr(a.status, (int32_t)status);
 }
 
-// The values of E codes (of E / 2 bytes for BPE_UINT4).
+// The values of E codes (of E / 2 bytes for BPE_UINT4: the lower and the upper
+// halves apart, since a byte to a float is one instruction).
 template <int F, typename T>
 __device__ __forceinline__ Vec<T, E> decode(const uint32_t *w, float scale, float low) {
   Vec<T, E> r;
+  uint32_t b[2];
+  if (F == BPE_UINT4) {
+    b[0] = w[0] & 0x0f0f0f0fu;
+    b[1] = w[0] >> 4 & 0x0f0f0f0fu;
+  }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     float y;
@@ -170,17 +244,36 @@ __device__ __forceinline__ Vec<T, E> decode(const uint32_t *w, float scale, floa
     } else if (F == BPE_INT8) {
       y = (float)(int8_t)(w[e >> 2] >> 8 * (e & 3)) * scale;
     } else {
-      y = fmaf((float)(w[0] >> 4 * e & 15), scale, low);
+      y = fmaf((float)(b[e & 1] >> 8 * (e >> 1) & 0xffu), scale, low);
     }
     r.v[e] = from_f32<T>(y);
   }
   return r;
 }
 
+// The codes of m (1 to E) elements; zeros behind them.
+template <int F, bool WHOLE>
+__device__ __forceinline__ void load_codes(const uint8_t *q, int m, uint32_t *w) {
+  if (WHOLE || m >= E) {
+    if (F == BPE_UINT4) {
+      w[0] = *(const b4 *)q;
+    } else {
+      const b8 x = *(const b8 *)q;
+      w[0] = x.x;
+      w[1] = x.y;
+    }
+    return;
+  }
+  w[0] = w[1] = 0;
+#pragma unroll
+  for (int e = 0; e < (F == BPE_UINT4 ? E / 2 : E); ++e)
+    if ((F == BPE_UINT4 ? 2 * e : e) < m) w[e >> 2] |= (uint32_t)q[e] << 8 * (e & 3);
+}
+
 // A workgroup has up to 64 tokens in a row of the packed batch.  Their slots
 // first, a lane each: the request by the offsets, the block by the table.  Then
 // the tokens' vectors side by side.
-template <typename T, int F>
+template <typename T, int F, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
   constexpr int64_t kNot = INT64_MIN;  // no request's
   __shared__ int64_t slots[kCacheTokens];
@@ -216,45 +309,65 @@ __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
   }
   __syncthreads();
   const int count = tokens * a.per_token.d;
-  for (int i = tid; i < count; i += CT) {
-    const int token = divide(a.per_token, i);
-    const int k = i - token * a.per_token.d;
-    const int head = divide(a.per_head, k);
-    const int c = (k - head * a.per_head.d) * E;
-    const int m = a.c.dim - c;
-    const int64_t slot = slots[token];
-    if (slot == kNot) continue;
-    Vec<T, E> y = {};
-    if (slot >= 0) {
-      const uint8_t *q = (const uint8_t *)a.c.codes + slot * a.c.codes_stride +
-                         (int64_t)head * a.row_bytes;
-      constexpr int B = F == BPE_UINT4 ? E / 2 : E;
-      Vec<uint8_t, B> w = {};
-      q += F == BPE_UINT4 ? c / 2 : c;
-      const int bytes = F == BPE_UINT4 ? (m + 1) / 2 : m;
+  constexpr int U = 4;
+  for (int base = 0; base < count; base += CT * U) {
+    // All loads first, unconditional ones, so that they are in flight together.
+    int64_t at[U], slot[U];
+    int m[U];
+    uint32_t w[U][2];
+    float scale[U], low[U];
 #pragma unroll
-      for (int e = 0; e < B; ++e)
-        if (e < bytes) w.v[e] = q[e];
-      uint32_t ww[2] = {};
-      __builtin_memcpy(ww, &w, B);
-      const float *s = a.c.scales + slot * a.c.scales_stride +
-                       ((int64_t)head * a.groups + (c >> a.group_log2)) * (F == BPE_UINT4 ? 2 : 1);
-      y = decode<F, T>(ww, s[0], F == BPE_UINT4 ? s[1] : 0.f);
+    for (int u = 0; u < U; ++u) {
+      const int i = min(base + u * CT + tid, count - 1);
+      const int token = divide(a.per_token, i);
+      const int k = i - token * a.per_token.d;
+      const int head = divide(a.per_head, k);
+      const int c = (k - head * a.per_head.d) * E;
+      m[u] = a.c.dim - c;
+      slot[u] = slots[token];
+      at[u] = (t0 + token) * a.t_stride + head * a.h_stride + c;
+      const uint8_t *q = (const uint8_t *)a.c.codes + slot[u] * a.c.codes_stride +
+                         (head * a.row_bytes + (F == BPE_UINT4 ? c >> 1 : c));
+      const float *s = a.c.scales + slot[u] * a.c.scales_stride +
+                       (head * a.groups + (c >> a.group_log2)) * (F == BPE_UINT4 ? 2 : 1);
+      const bool there = slot[u] >= 0;
+      load_codes<F, WHOLE>(there ? q : (const uint8_t *)a.off, m[u], w[u]);
+      if (!there) s = (const float *)a.off;
+      scale[u] = s[0];
+      low[u] = F == BPE_UINT4 ? s[1] : 0.f;
     }
-    store_some((T *)a.out + (t0 + token) * a.t_stride + head * a.h_stride + c, y, m);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      Vec<T, E> y = decode<F, T>(w[u], scale[u], low[u]);
+      if (slot[u] < 0) y = Vec<T, E>{};
+      if (base + u * CT + tid >= count || slot[u] == kNot) continue;
+      T *out = (T *)a.out + at[u];
+      if (WHOLE) store_vec<T, E, STREAM>(out, y);
+      else store_some(out, y, m[u]);
+    }
   }
   if (status) atomicOr(a.status, (int32_t)status);
 }
 
 template <typename T, int F>
 hipError_t write_launch(const CacheArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_cache_write<T, F>), dim3((unsigned)cache_workgroups(a)), dim3(CT), 0, stream, a);
+  const dim3 grid((unsigned)cache_workgroups(a)), wg(CT);
+  if (a.c.dim % E == 0) hipLaunchKernelGGL((k_cache_write<T, F, true>), grid, wg, 0, stream, a);
+  else hipLaunchKernelGGL((k_cache_write<T, F, false>), grid, wg, 0, stream, a);
+  return hipGetLastError();
+}
+template <typename T, int F, bool WHOLE>
+hipError_t read_launch(const CacheArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)cache_workgroups(a)), wg(CT);
+  if (a.n * a.c.heads * a.c.dim * (int64_t)sizeof(T) >= kStreamBytes)
+    hipLaunchKernelGGL((k_cache_read<T, F, WHOLE, true>), grid, wg, 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_cache_read<T, F, WHOLE, false>), grid, wg, 0, stream, a);
   return hipGetLastError();
 }
 template <typename T, int F>
-hipError_t read_launch(const CacheArgs &a, hipStream_t stream) {
-  hipLaunchKernelGGL((k_cache_read<T, F>), dim3((unsigned)cache_workgroups(a)), dim3(CT), 0, stream, a);
-  return hipGetLastError();
+hipError_t read_whole(const CacheArgs &a, hipStream_t stream) {
+  return a.c.dim % E == 0 ? read_launch<T, F, true>(a, stream) : read_launch<T, F, false>(a, stream);
 }
 
 template <typename T>
@@ -265,9 +378,9 @@ hipError_t write_as(const CacheArgs &a, hipStream_t stream) {
 }
 template <typename T>
 hipError_t read_as(const CacheArgs &a, hipStream_t stream) {
-  if (a.c.format == BPE_E4M3) return read_launch<T, BPE_E4M3>(a, stream);
-  if (a.c.format == BPE_INT8) return read_launch<T, BPE_INT8>(a, stream);
-  return read_launch<T, BPE_UINT4>(a, stream);
+  if (a.c.format == BPE_E4M3) return read_whole<T, BPE_E4M3>(a, stream);
+  if (a.c.format == BPE_INT8) return read_whole<T, BPE_INT8>(a, stream);
+  return read_whole<T, BPE_UINT4>(a, stream);
 }
 
 }  // namespace
