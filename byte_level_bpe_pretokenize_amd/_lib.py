@@ -22,7 +22,7 @@ SYMBOLS = (
 LM_SYMBOLS = (
     "bpe_embed_workspace_bytes", "bpe_embed", "bpe_embed_grad_workspace_bytes", "bpe_embed_grad", "bpe_process_logits",
     "bpe_block_tables_workspace_bytes", "bpe_block_tables", "bpe_cache_write", "bpe_cache_read",
-    "bpe_verify_drafts", "bpe_distill", "bpe_distill_grad",
+    "bpe_verify_drafts_workspace_bytes", "bpe_verify_drafts", "bpe_distill", "bpe_distill_grad",
 )
 
 BPE_OK, BPE_EINVAL, BPE_EMERGES, BPE_EIDMAP, BPE_EWORKSPACE, BPE_EHIP, BPE_ENOMEM, BPE_ENOTSUP, \
@@ -144,7 +144,9 @@ def load() -> C.CDLL:
     L.bpe_cache_write.restype = i32
     L.bpe_cache_read.argtypes = [C.POINTER(Cache), p, i64, i64, i64, i32, p, p, i64, p, i32, i64, i64, p, p]
     L.bpe_cache_read.restype = i32
-    L.bpe_verify_drafts.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, i64, p, p, p, p, p, p]
+    L.bpe_verify_drafts_workspace_bytes.argtypes = [i64, i64]
+    L.bpe_verify_drafts_workspace_bytes.restype = sz
+    L.bpe_verify_drafts.argtypes = [p, i32, i64, i64, i64, p, i64, p, p, i64, p, p, p, p, p, sz, p, p]
     L.bpe_verify_drafts.restype = i32
     L.bpe_distill.argtypes = [p, i32, i64, i64, i64, p, i64, p, i32, i64, i64, f32, p, p, p, p]
     L.bpe_distill.restype = i32

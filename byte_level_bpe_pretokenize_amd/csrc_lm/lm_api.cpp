@@ -279,20 +279,36 @@ int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_req
   return launch_cache_read(a, out_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }
 
+size_t bpe_verify_drafts_workspace_bytes(int64_t n_requests, int64_t vocab) {
+  if (n_requests <= 0 || n_requests >= (1 << 20) || verify_alone(n_requests, vocab) || vocab > BPE_MAX_ROWS)
+    return 0;
+  return (size_t)n_requests * (verify_regions(vocab) * 8 + 4);
+}
+
 int bpe_verify_drafts(const void *d_target, int prob_type, int64_t n_rows, int64_t vocab,
                       int64_t target_stride, const void *d_draft, int64_t draft_stride,
                       const int32_t *d_draft_ids, const int64_t *d_row_off, int64_t n_requests,
                       const float *d_accept, const float *d_sample, int32_t *d_tokens,
-                      int32_t *d_counts, int32_t *d_status, void *hip_stream) {
+                      int32_t *d_counts, void *d_workspace, size_t workspace_bytes,
+                      int32_t *d_status, void *hip_stream) {
   if (!type_ok(prob_type) || n_rows < 0 || n_rows > BPE_MAX_IDS || vocab < 1 ||
       vocab > BPE_MAX_ROWS || !stride_ok(target_stride, vocab) ||
       (d_draft && !stride_ok(draft_stride, vocab)) || n_requests < 0 ||
-      !launch_fits(n_requests, kVerifyThreads) || !d_status ||
+      n_requests >= (1 << 20) || !d_status ||
       (n_rows > 0 && (!d_target || !d_draft_ids || !d_accept || !d_tokens)) ||
       (n_requests > 0 && (!d_row_off || !d_sample || !d_counts)))
     return BPE_EINVAL;
   if (n_requests == 0) return BPE_OK;
   VerifyArgs a = {};
+  if (!verify_alone(n_requests, vocab)) {
+    if (workspace_bytes < bpe_verify_drafts_workspace_bytes(n_requests, vocab)) return BPE_EWORKSPACE;
+    if (!d_workspace || ((uintptr_t)d_workspace & 7)) return BPE_EINVAL;
+    a.sums = (double *)d_workspace;
+    a.rows = (int32_t *)(a.sums + n_requests * verify_regions(vocab));
+    if (!launch_fits(verify_workgroups(n_requests, vocab), kVerifyThreads)) return BPE_EINVAL;
+  }
+  a.regions = verify_regions(vocab);
+  a.tiles = verify_tiles(vocab);
   a.target = d_target;
   a.draft = d_draft;
   a.n_rows = n_rows;

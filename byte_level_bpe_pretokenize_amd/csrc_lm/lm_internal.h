@@ -221,7 +221,12 @@ hipError_t launch_cache_write(const CacheArgs &a, int xt, hipStream_t stream);
 hipError_t launch_cache_read(const CacheArgs &a, int ot, hipStream_t stream);
 
 // ---- drafted tokens -----------------------------------------------------------------
-constexpr int kVerifyThreads = 1024;  // a workgroup per request
+// A row is added up by regions of `tiles` tiles, four regions a wave.
+constexpr int kVerifyTile = 512;
+constexpr int kVerifyMostRegions = 4096;
+constexpr int kVerifyThreads = 256;
+constexpr int64_t kVerifyAlone = 65536;   // tokens that one workgroup adds up and draws from, at most
+constexpr int kVerifyAloneThreads = 768;
 
 struct VerifyArgs {
   const void *target, *draft;
@@ -231,8 +236,15 @@ struct VerifyArgs {
   int64_t R;
   const float *accept, *sample;
   int32_t *tokens, *counts, *status;
+  double *sums;   // [R][regions] workspace
+  int32_t *rows;  // [R] workspace: the row to draw from
+  int32_t regions, tiles;
 };
 
+bool verify_alone(int64_t n_requests, int64_t vocab);
+int32_t verify_regions(int64_t vocab);  // a multiple of 4
+int32_t verify_tiles(int64_t vocab);
+int64_t verify_workgroups(int64_t n_requests, int64_t vocab);
 hipError_t launch_verify(const VerifyArgs &a, int type, hipStream_t stream);
 
 // ---- distillation -------------------------------------------------------------------

@@ -157,6 +157,34 @@ void cache_shape(CacheArgs *a, bool write) {
   a->tokens = tokens < 1 ? 1 : tokens > kCacheTokens ? kCacheTokens : tokens;
 }
 
+// Whether a workgroup per request adds up its row and draws from it, in one launch
+// instead of two: while each has a CU of its own, up to where one CU's share of the
+// bandwidth costs what the second launch does; for more requests in small
+// vocabularies.  float32 with a draft's probabilities, one launch and two, us a
+// call from the host (captured in a graph): 4 requests of 50,256 tokens 11.8 and
+// 14.7 (11.9 and 8.3), 256 of them 20.5 and 22.7 (21.2 and 23.4), 256 of 32,256
+// 15.3 and 17.9 (16.2 and 18.6); 400 of 16,000 16.9 and 16.1, 800 of 8,000 15.2 and
+// 16.1, 800 of 16,000 33.5 and 23.9.
+bool verify_alone(int64_t n_requests, int64_t vocab) {
+  return vocab <= (n_requests <= 256 ? kVerifyAlone : 8192);
+}
+
+int32_t verify_regions(int64_t vocab) {
+  const int64_t four = (vocab + 4 * kVerifyTile - 1) / (4 * kVerifyTile) * 4;
+  return (int32_t)(four < kVerifyMostRegions ? four : kVerifyMostRegions);
+}
+
+int32_t verify_tiles(int64_t vocab) {
+  const int64_t per = (int64_t)verify_regions(vocab) * kVerifyTile;
+  return (int32_t)((vocab + per - 1) / per);
+}
+
+// Workgroups of the sums: a wave per four regions.
+int64_t verify_workgroups(int64_t n_requests, int64_t vocab) {
+  const int64_t per = kVerifyThreads / 16;
+  return n_requests * ((verify_regions(vocab) + per - 1) / per);
+}
+
 // Whether the gradient is one launch.
 bool distill_grad_fits(int64_t n_rows, int64_t vocab) {
   return launch_fits((vocab + kDistillSlab - 1) / kDistillSlab * n_rows, kDistillThreads);

@@ -470,6 +470,20 @@ def empty_cache(n_slots: int, heads: int, dim: int, dtype: torch.dtype = torch.f
     return codes.view(dtype), scales, group
 
 
+def _slots(t: torch.Tensor, row: int, what: str) -> int:
+    """The stride of a cache's slots, each of `row` consecutive elements."""
+    if t.is_contiguous():
+        return row
+    if t.numel() and not t[0].is_contiguous():
+        raise ValueError(f"{what}: expected slots of consecutive elements")
+    if t.shape[0] > 1:
+        s = t.stride(0)
+        if s < row:
+            raise ValueError(f"{what}: expected slots that do not overlap")
+        return s
+    return row
+
+
 def _cache(codes: torch.Tensor, scales: torch.Tensor, group: int, heads: int, dim: int):
     """bpe_cache of a cache's tensors."""
     form = _FORMATS.get(codes.dtype)
@@ -477,36 +491,34 @@ def _cache(codes: torch.Tensor, scales: torch.Tensor, group: int, heads: int, di
         raise TypeError(f"codes: float8_e4m3fn, int8 or uint8 expected, got {codes.dtype}")
     if scales.dtype is not torch.float32:
         raise TypeError(f"scales: torch.float32 expected, got {scales.dtype}")
-    group = _int32(group, 1, "group")
+    if group < 1:
+        raise ValueError(f"group: {group} is out of range")
     n = codes.shape[0]
-    row = (heads, dim if form != _lib.UINT4 else (dim + 1) // 2)
-    if tuple(codes.shape[1:]) != row:
-        raise ValueError(f"codes: (slots, {row[0]}, {row[1]}) expected, got {tuple(codes.shape)}")
-    G = -(-dim // group)
-    srow = (heads, G) if form != _lib.UINT4 else (heads, G, 2)
-    if scales.shape[0] != n or tuple(scales.shape[1:]) != srow:
-        raise ValueError(f"scales: {(n, *srow)} expected, got {tuple(scales.shape)}")
-    cs, ss = row[0] * row[1], heads * G * (2 if form == _lib.UINT4 else 1)
-    if n:
-        if not codes[0].is_contiguous() or not scales[0].is_contiguous():
-            raise ValueError("codes, scales: expected slots of consecutive elements")
-        if n > 1:
-            if codes.stride(0) < cs or scales.stride(0) < ss:
-                raise ValueError("codes, scales: expected slots that do not overlap")
-            cs, ss = codes.stride(0), scales.stride(0)
-    return _lib.Cache(codes.data_ptr() if n else None, scales.data_ptr() if n else None, n, cs, ss,
-                      heads, dim, group, form)
+    G = (dim + group - 1) // group
+    if form == _lib.UINT4:
+        width, per, want = (dim + 1) // 2, heads * G * 2, (n, heads, G, 2)
+    else:
+        width, per, want = dim, heads * G, (n, heads, G)
+    if codes.shape != (n, heads, width):
+        raise ValueError(f"codes: (slots, {heads}, {width}) expected, got {tuple(codes.shape)}")
+    if scales.shape != want:
+        raise ValueError(f"scales: {want} expected, got {tuple(scales.shape)}")
+    return _lib.Cache(codes.data_ptr(), scales.data_ptr(), n, _slots(codes, heads * width, "codes"),
+                      _slots(scales, per, "scales"), heads, dim, group, form)
 
 
 def _tokens(t: torch.Tensor, what: str):
     """(token stride, head stride) of (n, heads, dim) whose heads are consecutive
-    elements; 0 where there is one token or one head."""
+    elements; what one token or one head has is not looked at."""
     n, H, D = t.shape
-    if D > 1 and t.stride(2) != 1:
+    ts, hs, es = t.stride()
+    if es != 1 and D > 1:
         raise ValueError(f"{what}: expected heads of consecutive elements")
-    ts, hs = t.stride(0) if n > 1 else 0, t.stride(1) if H > 1 else 0
-    if (n > 1 and ts < D) or (H > 1 and hs < D) or \
-            (n > 1 and H > 1 and ts < (H - 1) * hs + D and hs < (n - 1) * ts + D):
+    if n > 1 and H > 1:
+        fits = ts >= (H - 1) * hs + D and hs >= D or hs >= (n - 1) * ts + D and ts >= D
+    else:
+        fits = (n <= 1 or ts >= D) and (H <= 1 or hs >= D)
+    if not fits:
         raise ValueError(f"{what}: expected heads that do not overlap")
     return ts, hs
 
@@ -591,10 +603,15 @@ def cache_read(codes: torch.Tensor, scales: torch.Tensor, group: int, table: tor
     return res
 
 
+def verify_drafts_workspace_bytes(n_requests: int, vocab: int) -> int:
+    return int(_lib.load().bpe_verify_drafts_workspace_bytes(n_requests, vocab))
+
+
 def verify_drafts(target: torch.Tensor, draft_ids: torch.Tensor, row_off: torch.Tensor,
                   accept: torch.Tensor, sample: torch.Tensor, *, draft: torch.Tensor | None = None,
                   tokens: torch.Tensor | None = None, counts: torch.Tensor | None = None,
-                  status: torch.Tensor | None = None, stream=None):
+                  workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                  stream=None):
     """bpe_verify_drafts: (tokens int32 (N), counts int32 (R)), new or the tensors
     given: each request's drafted tokens that stand and the one drawn after them,
     then -1, in its rows; and how many it got.
@@ -603,9 +620,10 @@ def verify_drafts(target: torch.Tensor, draft_ids: torch.Tensor, row_off: torch.
     rows, one more than their drafts.  draft_ids int32 (N): the token that a row
     verifies (its request's last row: anything); draft (N, V): the probabilities it
     was drawn from, None where the drafts were certain.  accept float32 (N), sample
-    float32 (R): uniform in [0, 1)."""
+    float32 (R): uniform in [0, 1).  ``workspace``: a contiguous device tensor of
+    verify_drafts_workspace_bytes bytes, allocated by the call when left out."""
     if stream is not None:
-        kw = dict(draft=draft, tokens=tokens, counts=counts, status=status)
+        kw = dict(draft=draft, tokens=tokens, counts=counts, workspace=workspace, status=status)
         return _on(stream, verify_drafts, (target, draft_ids, row_off, accept, sample, *kw.values()),
                    target, draft_ids, row_off, accept, sample, **kw)
     _no_gradient("verify_drafts", "call it ", (target, draft, accept, sample))
@@ -630,15 +648,27 @@ def verify_drafts(target: torch.Tensor, draft_ids: torch.Tensor, row_off: torch.
         _list(tokens, torch.int32, N, "tokens")
     if counts is not None:
         _list(counts, torch.int32, R, "counts")
-    dev = _device("verify_drafts", (target, draft, draft_ids, row_off, accept, sample, tokens, counts, status))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    dev = _device("verify_drafts", (target, draft, draft_ids, row_off, accept, sample, tokens, counts,
+                  workspace, status))
+    L = _lib.load()
     st = _status(status, dev)
     filled = [t for t in (tokens, counts) if t is not None]
     if tokens is None:
         tokens = draft_ids.new_empty(N)
     if counts is None:
         counts = draft_ids.new_empty(R)
-    rc = _lib.load().bpe_verify_drafts(target.data_ptr(), pt, N, V, ps, qp, qs, ip, op, R, ap, sp,
-                                       tokens.data_ptr(), counts.data_ptr(), st.data_ptr(), _stream(dev))
+    if workspace is None:
+        w_bytes = L.bpe_verify_drafts_workspace_bytes(R, V)
+        if w_bytes:  # (a float32 tensor of the inputs' device costs less than one of bytes)
+            workspace = sample.new_empty((w_bytes + 3) // 4)
+    else:
+        w_bytes = workspace.numel() * workspace.element_size()
+    rc = L.bpe_verify_drafts(target.data_ptr(), pt, N, V, ps, qp, qs, ip, op, R, ap, sp,
+                             tokens.data_ptr(), counts.data_ptr(),
+                             None if workspace is None else workspace.data_ptr(), w_bytes,
+                             st.data_ptr(), _stream(dev))
     if filled:
         _modified(filled)
     _end("bpe_verify_drafts", rc, st if status is None else None)

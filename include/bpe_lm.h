@@ -293,6 +293,10 @@ int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_req
                    int out_type, int64_t token_stride, int64_t head_stride, int32_t *d_status,
                    void *hip_stream);
 
+/* Workspace bytes bpe_verify_drafts needs (0 for small vocabularies, for few
+ * requests in larger ones, and for sizes out of range). */
+size_t bpe_verify_drafts_workspace_bytes(int64_t n_requests, int64_t vocab);
+
 /*
  * Which of a request's drafted tokens stand, and the token that follows them, so
  * that what comes out is distributed as the target alone would draw it.
@@ -320,14 +324,18 @@ int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_req
  * [0, n_rows] set BPE_STATUS_BAD_ID_OFFSETS, and their request counts as one
  * without rows.  Where there is nothing to draw from
  * (BPE_STATUS_NO_TOKEN) the next token is -1 and not counted.
- * n_rows <= 2^30, vocab <= BPE_MAX_ROWS, n_requests < 2^22.
- * Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
+ * d_workspace: device scratch, 8-byte aligned, of workspace_bytes >=
+ * bpe_verify_drafts_workspace_bytes(n_requests, vocab) (NULL where that is 0).
+ * n_rows <= 2^30, vocab <= BPE_MAX_ROWS, n_requests < 2^20, n_requests *
+ * min(256, ceil(vocab / 8192)) < 2^24.
+ * Returns BPE_OK, BPE_EINVAL, BPE_EWORKSPACE or BPE_EHIP.
  */
 int bpe_verify_drafts(const void *d_target, int prob_type, int64_t n_rows, int64_t vocab,
                       int64_t target_stride, const void *d_draft, int64_t draft_stride,
                       const int32_t *d_draft_ids, const int64_t *d_row_off, int64_t n_requests,
                       const float *d_accept, const float *d_sample, int32_t *d_tokens,
-                      int32_t *d_counts, int32_t *d_status, void *hip_stream);
+                      int32_t *d_counts, void *d_workspace, size_t workspace_bytes,
+                      int32_t *d_status, void *hip_stream);
 
 /*
  * The divergence of a student's distribution over the vocabulary from a

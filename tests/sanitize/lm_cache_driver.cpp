@@ -173,9 +173,26 @@ static void gradient() {
   CHECK(fits > 1000);
 }
 
+// A row's regions cover it, whole waves of them, and a launch that passes the checks
+// has fewer than 2^32 threads.
+static void regions() {
+  for (int i = 0; i < 100000; ++i) {
+    const int64_t V = i < 5000 ? i + 1 : 1 + below(i % 2 ? 300000 : BPE_MAX_ROWS);
+    const int64_t n = verify_regions(V), t = verify_tiles(V);
+    CHECK(n >= 4 && n % 4 == 0 && n <= kVerifyMostRegions && t >= 1);
+    CHECK(n * t * kVerifyTile >= V && (t == 1 || n == kVerifyMostRegions));
+    CHECK((n - 4) * t * kVerifyTile < V || t > 1);
+    for (int64_t r : {1, 256, 257, 100000})
+      if (verify_alone(r, V)) CHECK(n <= kVerifyAlone / kVerifyTile && t == 1);
+    const int64_t R = 1 + below(1 << 20), per = std::min<int64_t>(256, (V + 8191) / 8192);
+    CHECK(verify_workgroups(R, V) == R * per);
+    CHECK(launch_fits(verify_workgroups(R, V), kVerifyThreads) == (R * per < (int64_t)1 << 24));
+  }
+}
+
 int main(int argc, char **argv) {
   const std::pair<const char *, void (*)()> checks[] = {
-      {"shape", shape}, {"refusals", refusals}, {"request", request}, {"slot", slot}, {"gradient", gradient}};
+      {"shape", shape}, {"refusals", refusals}, {"request", request}, {"slot", slot}, {"gradient", gradient}, {"regions", regions}};
   for (const auto &c : checks)
     if (argc == 2 && !strcmp(argv[1], c.first)) {
       c.second();

@@ -6,7 +6,7 @@ import torch
 
 import lm_draft_reference as ref
 from lm_reference import f64
-from byte_level_bpe_pretokenize_amd import _lib, lm
+from byte_level_bpe_pretokenize_amd import BPEError, _lib, lm
 
 from gpu_util import device
 from test_gpu_lm import BF16, F16, F32, dev, gen, status, strided
@@ -46,7 +46,7 @@ def check(p, q, ids, off, accept, sample, bits=0):
 
 @pytest.mark.parametrize("with_draft", [True, False])
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
-@pytest.mark.parametrize("V", [1, 2, 7, 64, 255, 1000, 4096, 8192, 8193, 50257, 128256])
+@pytest.mark.parametrize("V", [1, 2, 7, 64, 255, 1000, 4096, 8192, 8193, 16384, 50257, 65536, 65537, 128256])
 def test_verify(V, dtype, with_draft):
     lengths = [0, 1, 5, 3, 0, 16, 2] if V < 100000 else [3, 0, 2]
     for seed in range(3 if V < 10000 else 1):
@@ -62,8 +62,9 @@ def test_verify_near_and_far(near):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-def test_verify_many(dtype):
-    check(*batch(list(np.random.default_rng(0).integers(0, 9, 700)), 500, dtype, 5))
+@pytest.mark.parametrize("R,V", [(700, 500), (256, 9000), (257, 8193), (300, 12000)])
+def test_verify_many(R, V, dtype):
+    check(*batch(list(np.random.default_rng(0).integers(0, 9 if V < 1000 else 2, R)), V, dtype, 5))
 
 
 def test_verify_more_drafts_than_threads():
@@ -78,7 +79,7 @@ def test_verify_more_drafts_than_threads():
     assert counts.tolist() == [1501, 1, 1024, 1025]
 
 
-@pytest.mark.parametrize("V", [5, 3000, 20000])
+@pytest.mark.parametrize("V", [5, 3000, 20000, 150000])
 def test_borders(V):
     """Probabilities of a power of two, whose sums are exact: a share that ends at a
     token's border goes to the next token, and u q = p does not stand."""
@@ -113,11 +114,12 @@ def test_samples_outside():
     assert got.tolist() == [1, 1, 4, 4, 4, 1]
 
 
-def test_what_is_no_probability():
+@pytest.mark.parametrize("V", [4000, 70000])
+def test_what_is_no_probability(V):
     """Negative entries, infinities and NaN count as 0; nothing left of the difference
     goes to the target's row; nothing at all gives no token."""
-    p = torch.rand((12, 4000), device=device(), generator=gen(1))
-    q = torch.rand((12, 4000), device=device(), generator=gen(2))
+    p = torch.rand((12, V), device=device(), generator=gen(1))
+    q = torch.rand((12, V), device=device(), generator=gen(2))
     for t in (p, q):
         t[:, ::5] = float("nan")
         t[:, 1::7] = float("inf")
@@ -205,6 +207,17 @@ def test_a_large_vocabulary():
         assert counts.tolist() == [1] and got.tolist() == [want, -1]
 
 
+def test_a_workspace_of_ones_own():
+    p, q, ids, off, accept, sample = batch([4, 1, 0, 7], 70000, BF16, 2)
+    want = lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q)
+    need = lm.verify_drafts_workspace_bytes(4, 70000)
+    ws = torch.full((need + 8,), 77, dtype=torch.uint8, device=device())
+    got = lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q, workspace=ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and bool((ws[need:] == 77).all())
+    with pytest.raises(BPEError):
+        lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q, workspace=ws[:need - 1])
+
+
 def test_the_distribution():
     """What comes out first is distributed as the target: 200,000 draws, each
     frequency within five deviations."""
@@ -222,7 +235,8 @@ def test_the_distribution():
 
 
 def test_captured_and_replayed():
-    p, q, ids, off, accept, sample = batch([4, 1, 0, 7], 5000, F32, 2)
+    V = 70000  # (a workspace)
+    p, q, ids, off, accept, sample = batch([4, 1, 0, 7], V, F32, 2)
     t_off, st = dev(off), status()
     tokens = torch.zeros(p.shape[0], dtype=torch.int32, device=device())
     counts = torch.zeros(4, dtype=torch.int32, device=device())
@@ -237,7 +251,7 @@ def test_captured_and_replayed():
     with torch.cuda.graph(graph):
         step()
     for k in range(4):
-        for t, x in zip((p, q, ids), batch([4, 1, 0, 7], 5000, F32, 10 + k)):
+        for t, x in zip((p, q, ids), batch([4, 1, 0, 7], V, F32, 10 + k)):
             t.copy_(x)
         accept.uniform_(generator=gen(k))
         sample.uniform_(generator=gen(k + 9))
@@ -250,8 +264,7 @@ def test_captured_and_replayed():
 
 
 def test_another_stream():
-    args = batch([4, 1, 0, 7], 5000, F32, 2)
-    p, q, ids, off, accept, sample = args
+    p, q, ids, off, accept, sample = batch([4, 1, 0, 7], 70000, F32, 2)
     want = lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q)
     side, st = torch.cuda.Stream(), status()
     busy = torch.ones((4096, 4096), device=device())

@@ -1,4 +1,4 @@
-"""What the host decides for a cache of few bits and for a loss's gradient, and the
+"""What the host decides for a cache of few bits, drafted tokens and a loss's gradient, and the
 searches that the cache's kernels make with a caller's offsets and tables, built
 for the CPU under AddressSanitizer and UndefinedBehaviorSanitizer:
 tests/sanitize/lm_cache_driver.cpp, one check per test."""
@@ -27,7 +27,7 @@ def driver(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("check", ["shape", "refusals", "request", "slot", "gradient"])
+@pytest.mark.parametrize("check", ["shape", "refusals", "request", "slot", "gradient", "regions"])
 def test_layout(driver, check):
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=1:verify_asan_link_order=0",
                UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")

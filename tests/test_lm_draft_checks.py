@@ -77,17 +77,34 @@ def test_cache_of_nothing():
 
 
 def verify_rc(target=P, pt=0, N=9, V=100, ps=100, draft=P, qs=100, ids=P, off=P, R=3, accept=P, sample=P,
-              tokens=P, counts=P, status=P):
+              tokens=P, counts=P, ws=None, ws_bytes=0, status=P):
     return _lib.load().bpe_verify_drafts(target, pt, N, V, ps, draft, qs, ids, off, R, accept, sample, tokens,
-                                         counts, status, None)
+                                         counts, ws, ws_bytes, status, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(target=None), dict(ids=None), dict(off=None), dict(accept=None), dict(sample=None), dict(tokens=None),
     dict(counts=None), dict(status=None), dict(pt=3), dict(N=-1), dict(V=0), dict(V=_lib.MAX_ROWS + 1, ps=1 << 28),
-    dict(ps=99), dict(qs=99), dict(R=-1), dict(R=1 << 22), dict(N=(1 << 30) + 1)])
+    dict(ps=99), dict(qs=99), dict(R=-1), dict(R=1 << 20), dict(N=(1 << 30) + 1)])
 def test_verify_refuses(bad):
     assert verify_rc(**bad) == EINVAL
+
+
+def test_verify_workspace():
+    assert lm.verify_drafts_workspace_bytes(1000, 768) == 0
+    assert lm.verify_drafts_workspace_bytes(0, 50000) == 0
+    assert lm.verify_drafts_workspace_bytes(256, 65536) == 0
+    big = dict(V=70000, ps=70000, qs=70000)
+    need = lm.verify_drafts_workspace_bytes(3, 70000)
+    assert 0 < need <= 3 * (8 * 70000 / 512 + 40)
+    assert verify_rc(**big, ws=P, ws_bytes=need - 1) == _lib.BPE_EWORKSPACE
+    assert verify_rc(**big, ws=None, ws_bytes=need) == EINVAL
+    assert verify_rc(**big, ws=P + 4, ws_bytes=need) == EINVAL
+    # the limit of the launch
+    R, V = 1 << 16, 1 << 21
+    assert verify_rc(V=V, ps=V, qs=V, R=R, ws=P, ws_bytes=1 << 50) == EINVAL
+    assert verify_rc(V=V, ps=V, qs=V, R=R - 1, ws=P, ws_bytes=0) == _lib.BPE_EWORKSPACE
+    assert verify_rc(V=_lib.MAX_ROWS, ps=_lib.MAX_ROWS, qs=_lib.MAX_ROWS, R=R, ws=P, ws_bytes=1 << 50) == EINVAL
 
 
 def test_verify_of_nothing():
@@ -191,6 +208,7 @@ def verify(target=None, ids=None, off=None, accept=None, sample=None, **kw):
     (ValueError, lambda: verify(draft=z(4, 51))),
     (ValueError, lambda: verify(tokens=z(3, dtype=I32))),
     (TypeError, lambda: verify(counts=z(2, dtype=I64))),
+    (ValueError, lambda: verify(workspace=z(4, 4).t())),
     (TypeError, lambda: lm.distill(z(3, 40, dtype=I32), z(3, 5, dtype=I32), z(3, 5))),
     (TypeError, lambda: lm.distill(z(3, 40), z(3, 5, dtype=I64), z(3, 5))),
     (ValueError, lambda: lm.distill(z(3, 40), z(3, 5, dtype=I32), z(3, 4))),
