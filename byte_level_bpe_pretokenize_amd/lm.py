@@ -82,6 +82,15 @@ def _rows(t: torch.Tensor, what: str) -> int:
     return m
 
 
+def _matrix(t: torch.Tensor, what: str):
+    """(rows, columns, row stride) of such a matrix."""
+    shape = t.shape
+    if len(shape) == 2:
+        n, m = shape
+        return n, m, m if t.is_contiguous() else _rows(t, what)
+    raise ValueError(f"{what}: expected a matrix, got {len(shape)} dimensions")
+
+
 def _int32(x: int, lo: int, what: str) -> int:
     if not lo <= x < 1 << 31:
         raise ValueError(f"{what}: {x} is out of range")
@@ -493,7 +502,7 @@ def _cache(codes: torch.Tensor, scales: torch.Tensor, group: int, heads: int, di
         raise TypeError(f"scales: torch.float32 expected, got {scales.dtype}")
     if group < 1:
         raise ValueError(f"group: {group} is out of range")
-    n = codes.shape[0]
+    shape, n = scales.shape, codes.shape[0]
     G = (dim + group - 1) // group
     if form == _lib.UINT4:
         width, per, want = (dim + 1) // 2, heads * G * 2, (n, heads, G, 2)
@@ -501,8 +510,8 @@ def _cache(codes: torch.Tensor, scales: torch.Tensor, group: int, heads: int, di
         width, per, want = dim, heads * G, (n, heads, G)
     if codes.shape != (n, heads, width):
         raise ValueError(f"codes: (slots, {heads}, {width}) expected, got {tuple(codes.shape)}")
-    if scales.shape != want:
-        raise ValueError(f"scales: {want} expected, got {tuple(scales.shape)}")
+    if shape != want:
+        raise ValueError(f"scales: {want} expected, got {tuple(shape)}")
     return _lib.Cache(codes.data_ptr(), scales.data_ptr(), n, _slots(codes, heads * width, "codes"),
                       _slots(scales, per, "scales"), heads, dim, group, form)
 
@@ -577,8 +586,7 @@ def cache_read(codes: torch.Tensor, scales: torch.Tensor, group: int, table: tor
     c = _cache(codes, scales, group, H, dim)
     if table.dtype is not torch.int32:
         raise TypeError(f"table: torch.int32 expected, got {table.dtype}")
-    tstr = _rows(table, "table")
-    R, W = table.shape
+    R, W, tstr = _matrix(table, "table")
     op = _list(off, torch.int64, R + 1, "off")
     fp = None if start is None else _list(start, torch.int32, R, "start")
     block_size = _int32(block_size, 1, "block_size")
@@ -594,7 +602,7 @@ def cache_read(codes: torch.Tensor, scales: torch.Tensor, group: int, table: tor
         ts, hs = _tokens(out, "out")
     dev = _device("cache_read", (codes, scales, table, off, start, out, status))
     st = _status(status, dev)
-    res = torch.empty((n, H, dim), dtype=dt, device=codes.device) if out is None else out
+    res = scales.new_empty(n, H, dim, dtype=dt) if out is None else out
     rc = _lib.load().bpe_cache_read(C.byref(c), table.data_ptr(), R, W, tstr, block_size, op, fp, n,
                                     res.data_ptr(), ot, ts, hs, st.data_ptr(), _stream(dev))
     if out is not None:
@@ -627,15 +635,15 @@ def verify_drafts(target: torch.Tensor, draft_ids: torch.Tensor, row_off: torch.
         return _on(stream, verify_drafts, (target, draft_ids, row_off, accept, sample, *kw.values()),
                    target, draft_ids, row_off, accept, sample, **kw)
     _no_gradient("verify_drafts", "call it ", (target, draft, accept, sample))
-    pt, ps = _type(target.dtype, "target"), _rows(target, "target")
-    N, V = target.shape
+    pt = _type(target.dtype, "target")
+    N, V, ps = _matrix(target, "target")
     R = row_off.numel() - 1
     qp, qs = None, 0
     if draft is not None:
         if draft.dtype is not target.dtype:
             raise TypeError(f"draft: {target.dtype} expected, got {draft.dtype}")
-        qs = _rows(draft, "draft")
-        if draft.shape != target.shape:
+        qn, qv, qs = _matrix(draft, "draft")
+        if qn != N or qv != V:
             raise ValueError(f"draft: {tuple(target.shape)} expected, got {tuple(draft.shape)}")
         qp = draft.data_ptr()
     ip = _list(draft_ids, torch.int32, N, "draft_ids")
@@ -677,16 +685,16 @@ def verify_drafts(target: torch.Tensor, draft_ids: torch.Tensor, row_off: torch.
 
 def _teacher(student, ids, teacher):
     """What a student's and a teacher's rows are passed as."""
-    zt, zs = _type(student.dtype, "student"), _rows(student, "student")
-    tt, ts = _type(teacher.dtype, "teacher"), _rows(teacher, "teacher")
+    N, V, zs = _matrix(student, "student")
+    n, K, is_ = _matrix(ids, "ids")
+    tn, tk, ts = _matrix(teacher, "teacher")
     if ids.dtype is not torch.int32:
         raise TypeError(f"ids: torch.int32 expected, got {ids.dtype}")
-    is_ = _rows(ids, "ids")
-    N, V = student.shape
-    if ids.shape != teacher.shape or ids.shape[0] != N:
+    if n != N or tn != N or tk != K:
         raise ValueError(f"ids, teacher: {N} rows of the same width expected, got {tuple(ids.shape)} "
                          f"and {tuple(teacher.shape)}")
-    return (student.data_ptr(), zt, N, V, zs, ids.data_ptr(), is_, teacher.data_ptr(), tt, ts, ids.shape[1])
+    return (student.data_ptr(), _type(student.dtype, "student"), N, V, zs, ids.data_ptr(), is_,
+            teacher.data_ptr(), _type(teacher.dtype, "teacher"), ts, K)
 
 
 def distill(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, temperature: float = 1.0,
@@ -715,7 +723,7 @@ def distill(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, tem
     if losses is None:
         losses = student.new_empty(N, dtype=torch.float32)
     if stats is None:
-        stats = student.new_empty((N, 4), dtype=torch.float32)
+        stats = student.new_empty(N, 4, dtype=torch.float32)
     rc = _lib.load().bpe_distill(*a, temperature, losses.data_ptr(), stats.data_ptr(), st.data_ptr(),
                                  _stream(dev))
     if filled:
@@ -750,7 +758,7 @@ def distill_grad(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
             raise ValueError(f"out: {tuple(student.shape)} of out_dtype expected, got {tuple(out.shape)}")
     dev = _device("distill_grad", (student, ids, teacher, stats, dloss, out, status))
     st = _status(status, dev)
-    res = student.new_empty((N, V), dtype=dt) if out is None else out
+    res = student.new_empty(N, V, dtype=dt) if out is None else out
     rc = _lib.load().bpe_distill_grad(*a, sp, dp, temperature, res.data_ptr(), ot, os_, st.data_ptr(),
                                       _stream(dev))
     if out is not None:
