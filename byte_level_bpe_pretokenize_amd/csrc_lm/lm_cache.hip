@@ -223,8 +223,11 @@ __global__ void __launch_bounds__(CT) k_cache_write(CacheArgs a) {
 
 // The values of E codes (of E / 2 bytes for BPE_UINT4: the lower and the upper
 // halves apart, since a byte to a float is one instruction).
-template <int F, typename T>
-__device__ __forceinline__ Vec<T, E> decode(const uint32_t *w, float scale, float low) {
+struct Step {
+  float scale, low;
+};
+template <int F, typename T, typename S>
+__device__ __forceinline__ Vec<T, E> decode(const uint32_t *w, S step) {
   Vec<T, E> r;
   uint32_t b[2];
   if (F == BPE_UINT4) {
@@ -234,40 +237,47 @@ __device__ __forceinline__ Vec<T, E> decode(const uint32_t *w, float scale, floa
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     float y;
+    const Step x = step(e);
     if (F == BPE_E4M3) {
       const int s = e & 3;
       y = s == 0   ? __builtin_amdgcn_cvt_f32_fp8(w[e >> 2], 0)
           : s == 1 ? __builtin_amdgcn_cvt_f32_fp8(w[e >> 2], 1)
           : s == 2 ? __builtin_amdgcn_cvt_f32_fp8(w[e >> 2], 2)
                    : __builtin_amdgcn_cvt_f32_fp8(w[e >> 2], 3);
-      y *= scale;
+      y *= x.scale;
     } else if (F == BPE_INT8) {
-      y = (float)(int8_t)(w[e >> 2] >> 8 * (e & 3)) * scale;
+      y = (float)(int8_t)(w[e >> 2] >> 8 * (e & 3)) * x.scale;
     } else {
-      y = fmaf((float)(b[e & 1] >> 8 * (e >> 1) & 0xffu), scale, low);
+      y = fmaf((float)(b[e & 1] >> 8 * (e >> 1) & 0xffu), x.scale, x.low);
     }
     r.v[e] = from_f32<T>(y);
   }
   return r;
 }
 
-// The codes of m (1 to E) elements; zeros behind them.
+// The codes of the E elements from c on of a head's row q; of BPE_UINT4 c may be odd
+// where they are the head's last.
 template <int F, bool WHOLE>
-__device__ __forceinline__ void load_codes(const uint8_t *q, int m, uint32_t *w) {
-  if (WHOLE || m >= E) {
-    if (F == BPE_UINT4) {
-      w[0] = *(const b4 *)q;
-    } else {
-      const b8 x = *(const b8 *)q;
-      w[0] = x.x;
-      w[1] = x.y;
+__device__ __forceinline__ void load_codes(const uint8_t *q, int c, uint32_t *w) {
+  if (F == BPE_UINT4) {
+    w[0] = *(const b4 *)(q + (c >> 1));
+    if (!WHOLE) {
+      const uint32_t after = q[(c + E - 1) >> 1];
+      if (c & 1) w[0] = w[0] >> 4 | after << 28;
     }
-    return;
+  } else {
+    const b8 x = *(const b8 *)(q + c);
+    w[0] = x.x;
+    w[1] = x.y;
   }
+}
+// Those of a head of dim < E elements.
+template <int F>
+__device__ __forceinline__ void load_few(const uint8_t *q, int dim, uint32_t *w) {
   w[0] = w[1] = 0;
 #pragma unroll
   for (int e = 0; e < (F == BPE_UINT4 ? E / 2 : E); ++e)
-    if ((F == BPE_UINT4 ? 2 * e : e) < m) w[e >> 2] |= (uint32_t)q[e] << 8 * (e & 3);
+    if ((F == BPE_UINT4 ? 2 * e : e) < dim) w[e >> 2] |= (uint32_t)q[e] << 8 * (e & 3);
 }
 
 // A workgroup has up to 64 tokens in a row of the packed batch.  Their slots
@@ -312,38 +322,47 @@ __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
   constexpr int U = 4;
   for (int base = 0; base < count; base += CT * U) {
     // All loads first, unconditional ones, so that they are in flight together.
+    // Heads of no whole vectors: the last vector is the head's last E elements, some
+    // of which the one before it has too (both store the same); it may have two
+    // groups' elements.
     int64_t at[U], slot[U];
-    int m[U];
+    int edge[U];  // the first element of the second group
     uint32_t w[U][2];
-    float scale[U], low[U];
+    Step first[U], second[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = min(base + u * CT + tid, count - 1);
       const int token = divide(a.per_token, i);
       const int k = i - token * a.per_token.d;
       const int head = divide(a.per_head, k);
-      const int c = (k - head * a.per_head.d) * E;
-      m[u] = a.c.dim - c;
+      int c = (k - head * a.per_head.d) * E;
+      if (!WHOLE) c = max(min(c, a.c.dim - E), 0);
       slot[u] = slots[token];
       at[u] = (t0 + token) * a.t_stride + head * a.h_stride + c;
-      const uint8_t *q = (const uint8_t *)a.c.codes + slot[u] * a.c.codes_stride +
-                         (head * a.row_bytes + (F == BPE_UINT4 ? c >> 1 : c));
-      const float *s = a.c.scales + slot[u] * a.c.scales_stride +
-                       (head * a.groups + (c >> a.group_log2)) * (F == BPE_UINT4 ? 2 : 1);
-      const bool there = slot[u] >= 0;
-      load_codes<F, WHOLE>(there ? q : (const uint8_t *)a.off, m[u], w[u]);
-      if (!there) s = (const float *)a.off;
-      scale[u] = s[0];
-      low[u] = F == BPE_UINT4 ? s[1] : 0.f;
+      const uint8_t *q = (const uint8_t *)a.c.codes + slot[u] * a.c.codes_stride + head * a.row_bytes;
+      const float *s = a.c.scales + slot[u] * a.c.scales_stride + head * a.groups * (F == BPE_UINT4 ? 2 : 1);
+      if (slot[u] < 0) {  // (any place that is there)
+        q = (const uint8_t *)a.off - (F == BPE_UINT4 ? c >> 1 : c);
+        s = (const float *)a.off - (c >> a.group_log2) * (F == BPE_UINT4 ? 2 : 1);
+      }
+      if (WHOLE || a.c.dim >= E) load_codes<F, WHOLE>(q, c, w[u]);
+      else load_few<F>(q, a.c.dim, w[u]);
+      const int g = c >> a.group_log2, h = WHOLE ? g : min(c + E - 1, a.c.dim - 1) >> a.group_log2;
+      auto load_step = [&](int g) {
+        return F == BPE_UINT4 ? Step{s[2 * g], s[2 * g + 1]} : Step{s[g], 0.f};
+      };
+      first[u] = load_step(g);
+      if (!WHOLE) second[u] = load_step(slot[u] < 0 ? g : h);
+      edge[u] = (h << a.group_log2) - c;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      Vec<T, E> y = decode<F, T>(w[u], scale[u], low[u]);
+      Vec<T, E> y = decode<F, T>(w[u], [&](int e) { return WHOLE || e < edge[u] ? first[u] : second[u]; });
       if (slot[u] < 0) y = Vec<T, E>{};
       if (base + u * CT + tid >= count || slot[u] == kNot) continue;
       T *out = (T *)a.out + at[u];
-      if (WHOLE) store_vec<T, E, STREAM>(out, y);
-      else store_some(out, y, m[u]);
+      if (WHOLE || a.c.dim >= E) store_vec<T, E, STREAM>(out, y);
+      else store_some(out, y, a.c.dim);
     }
   }
   if (status) atomicOr(a.status, (int32_t)status);
@@ -356,18 +375,17 @@ hipError_t write_launch(const CacheArgs &a, hipStream_t stream) {
   else hipLaunchKernelGGL((k_cache_write<T, F, false>), grid, wg, 0, stream, a);
   return hipGetLastError();
 }
-template <typename T, int F, bool WHOLE>
+template <typename T, int F>
 hipError_t read_launch(const CacheArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)cache_workgroups(a)), wg(CT);
-  if (a.n * a.c.heads * a.c.dim * (int64_t)sizeof(T) >= kStreamBytes)
-    hipLaunchKernelGGL((k_cache_read<T, F, WHOLE, true>), grid, wg, 0, stream, a);
+  const bool big = a.n * a.c.heads * a.c.dim * (int64_t)sizeof(T) >= kStreamBytes;
+  if (a.c.dim % E != 0)
+    hipLaunchKernelGGL((k_cache_read<T, F, false, false>), grid, wg, 0, stream, a);
+  else if (big)
+    hipLaunchKernelGGL((k_cache_read<T, F, true, true>), grid, wg, 0, stream, a);
   else
-    hipLaunchKernelGGL((k_cache_read<T, F, WHOLE, false>), grid, wg, 0, stream, a);
+    hipLaunchKernelGGL((k_cache_read<T, F, true, false>), grid, wg, 0, stream, a);
   return hipGetLastError();
-}
-template <typename T, int F>
-hipError_t read_whole(const CacheArgs &a, hipStream_t stream) {
-  return a.c.dim % E == 0 ? read_launch<T, F, true>(a, stream) : read_launch<T, F, false>(a, stream);
 }
 
 template <typename T>
@@ -378,9 +396,9 @@ hipError_t write_as(const CacheArgs &a, hipStream_t stream) {
 }
 template <typename T>
 hipError_t read_as(const CacheArgs &a, hipStream_t stream) {
-  if (a.c.format == BPE_E4M3) return read_whole<T, BPE_E4M3>(a, stream);
-  if (a.c.format == BPE_INT8) return read_whole<T, BPE_INT8>(a, stream);
-  return read_whole<T, BPE_UINT4>(a, stream);
+  if (a.c.format == BPE_E4M3) return read_launch<T, BPE_E4M3>(a, stream);
+  if (a.c.format == BPE_INT8) return read_launch<T, BPE_INT8>(a, stream);
+  return read_launch<T, BPE_UINT4>(a, stream);
 }
 
 }  // namespace
