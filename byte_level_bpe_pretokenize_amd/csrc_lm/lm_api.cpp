@@ -36,7 +36,7 @@ bool distill_ok(int student_type, int64_t n_rows, int64_t vocab, int64_t student
                 int64_t ids_stride, int teacher_type, int64_t teacher_stride, int64_t top,
                 float temperature) {
   return type_ok(student_type) && type_ok(teacher_type) && n_rows >= 0 &&
-         launch_fits(n_rows, kDistillWide) && vocab >= 1 && vocab <= BPE_MAX_ROWS &&
+         launch_fits(n_rows, kDistillThreads) && vocab >= 1 && vocab <= BPE_MAX_ROWS &&
          stride_ok(student_stride, vocab) && top >= 0 && top <= BPE_MAX_TOP &&
          stride_ok(ids_stride, top) && stride_ok(teacher_stride, top) && temperature >= 0x1p-20f &&
          temperature <= 0x1p20f;

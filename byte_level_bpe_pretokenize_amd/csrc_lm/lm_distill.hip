@@ -19,13 +19,37 @@ constexpr Soft kNothing = {-FLT_MAX, 0.f};
 
 __device__ __forceinline__ float power(float x, float k) { return __builtin_amdgcn_exp2f(x * k); }
 
-// The wave's, in every lane.
+// The largest of the wave's values and their sum, in every lane (every lane
+// active): six DPP moves each, as in wave_incl_sum.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float moved(float old, float x) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), CTRL, ROW_MASK, 0xF, false));
+}
+__device__ __forceinline__ float lane63(float x) {
+  return __int_as_float(lane_value(__float_as_int(x), 63));
+}
+__device__ __forceinline__ float wave_largest(float x) {
+  x = fmaxf(x, moved<0x111, 0xF>(x, x));
+  x = fmaxf(x, moved<0x112, 0xF>(x, x));
+  x = fmaxf(x, moved<0x114, 0xF>(x, x));
+  x = fmaxf(x, moved<0x118, 0xF>(x, x));
+  x = fmaxf(x, moved<0x142, 0xA>(x, x));
+  x = fmaxf(x, moved<0x143, 0xC>(x, x));
+  return lane63(x);
+}
+__device__ __forceinline__ float wave_total(float x) {
+  x += moved<0x111, 0xF>(0.f, x);
+  x += moved<0x112, 0xF>(0.f, x);
+  x += moved<0x114, 0xF>(0.f, x);
+  x += moved<0x118, 0xF>(0.f, x);
+  x += moved<0x142, 0xA>(0.f, x);
+  x += moved<0x143, 0xC>(0.f, x);
+  return lane63(x);
+}
 __device__ __forceinline__ Soft wave_soft(Soft x, float k) {
-  float m = x.m;
-  for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-  x.s = wave_sum(x.s * power(x.m - m, k));
-  x.m = m;
-  return x;
+  const float m = wave_largest(x.m);
+  return Soft{m, wave_total(x.s * power(x.m - m, k))};
 }
 
 // An entry of a teacher's row: its token's place, or -1.
@@ -104,16 +128,14 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   }
   x = wave_soft(x, k);
   t = wave_soft(t, k);
-  if (lane == 0) {
-    soft_z[wave] = x;
-    soft_t[wave] = t;
-  }
-  __syncthreads();
   if (W > 1) {
-    x = lane < W ? soft_z[lane] : kNothing;
-    t = lane < W ? soft_t[lane] : kNothing;
-    x = wave_soft(x, k);
-    t = wave_soft(t, k);
+    if (lane == 0) {
+      soft_z[wave] = x;
+      soft_t[wave] = t;
+    }
+    __syncthreads();
+    x = wave_soft(lane < W ? soft_z[lane] : kNothing, k);
+    t = wave_soft(lane < W ? soft_t[lane] : kNothing, k);
   }
   const double by = 1.0 / (double)a.temperature;
   double sum = 0.0;
@@ -125,11 +147,15 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     if (e != 0.f) sum += (double)e * (((double)y.t - t.m) - ((double)zj - x.m));
   }
   sum = wave_sum(sum);
-  if (lane == 0) terms[wave] = sum;
-  __syncthreads();
+  if (W > 1) {
+    if (lane == 0) terms[wave] = sum;
+    __syncthreads();
+  }
   if (tid == 0) {
-    sum = 0.0;
-    for (int w = 0; w < W; ++w) sum += terms[w];
+    if (W > 1) {
+      sum = 0.0;
+      for (int w = 0; w < W; ++w) sum += terms[w];
+    }
     const bool some = x.s != 0.f && t.s != 0.f;
     const double T = a.temperature;
     a.losses[n] = some ? (float)(T * T * (sum * by / t.s + log((double)x.s) - log((double)t.s))) : 0.f;
@@ -144,16 +170,19 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
 
 // A workgroup per row and slab of logits: all of them as if nothing were listed,
 // then the listed ones of the slab again.  (Few are listed: asked for at every
-// logit they would cost more.)  A token listed twice gets the same value from
-// both entries: each adds up all of the token's, in their order.
-template <typename TS, typename TT, typename TG>
-__global__ void __launch_bounds__(kDistillThreads) k_distill_grad(DistillArgs a) {
-  constexpr int NT = kDistillThreads, S = kDistillSlab;
+// logit they would cost more.)  A token that is listed twice gets the same value
+// from both entries: each adds up all of the token's, in their order.  Which ones
+// are is known from two bits for each of the slab's logits: listed, and listed by
+// another entry too.
+template <typename TS, typename TT, typename TG, int NT, int S, bool STREAM>
+__global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   constexpr int E = sizeof(TS) == 2 && sizeof(TG) == 2 ? 8 : 4;
   constexpr int U = 4;
-  constexpr int PER = BPE_MAX_TOP / NT;
-  __shared__ int32_t ids[BPE_MAX_TOP];
-  __shared__ float parts[BPE_MAX_TOP];
+  __shared__ uint32_t seen[S / 32], twice[S / 32];
+  extern __shared__ __align__(16) int32_t lds[];
+  const int top8 = (a.top + 7) / 8 * 8;
+  int32_t *ids = lds;
+  float *parts = (float *)(ids + top8), *listed = parts + top8;  // (their logits)
   const int tid = threadIdx.x;
   const uint32_t slabs = (uint32_t)((a.vocab + S - 1) / S);
   const uint32_t row = blockIdx.x / slabs, slab = blockIdx.x - row * slabs;
@@ -169,26 +198,18 @@ __global__ void __launch_bounds__(kDistillThreads) k_distill_grad(DistillArgs a)
   const float c = some ? a.dloss[n] * a.temperature : 0.f;
   const float by_zs = 1.f / zs, by_ts = 1.f / ts;
   auto share = [&](float x) { return power(x - zm, k) * by_zs; };
-  // this thread's entries in the slab: their places and logits
-  int at[PER];
-  float zj[PER];
+  // an entry's place in the slab, or a number past it
+  auto place = [&](int32_t id) { return (uint32_t)id - (uint32_t)v0; };
   bool bad = false;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int j = tid + i * NT;
-    at[i] = -1;
-    if (j < a.top) {
-      const Entry y = load_entry<TT>(a, n, j);
-      bad |= y.id < -1 || y.id >= a.vocab;
-      ids[j] = y.id;
-      parts[j] = y.id >= 0 ? power(y.t - tm, k) * by_ts : 0.f;
-      const uint32_t p = (uint32_t)y.id - (uint32_t)v0;
-      if (some && p < (uint32_t)count) {
-        at[i] = (int)p;
-        zj[i] = (float)z[p];
-      }
-    }
+  // (the list is filled up to whole groups of 8 with entries that hold no token)
+  for (int j = tid; j < top8; j += NT) {
+    const Entry y = load_entry<TT>(a, n, j);
+    bad |= y.id < -1 || y.id >= a.vocab;
+    ids[j] = y.id;
+    parts[j] = y.id >= 0 ? power(y.t - tm, k) * by_ts : 0.f;
+    if (place(y.id) < (uint32_t)count) listed[j] = (float)z[place(y.id)];
   }
+  for (int i = tid; i < S / 32; i += NT) seen[i] = twice[i] = 0;
   if (bad && slab == 0) atomicOr(a.status, BPE_STATUS_BAD_ID);
   auto gradient = [&](const Vec<TS, E> &x) {
     Vec<TG, E> y;
@@ -196,42 +217,60 @@ __global__ void __launch_bounds__(kDistillThreads) k_distill_grad(DistillArgs a)
     for (int e = 0; e < E; ++e) y.v[e] = from_f32<TG>(some ? c * share((float)x.v[e]) : 0.f);
     return y;
   };
+  // (the barrier: the listed logits are read before any is overwritten)
+  auto claim = [&] {
+    __syncthreads();
+    for (int j = tid; j < a.top; j += NT) {
+      const uint32_t at = place(ids[j]), bit = 1u << (at & 31);
+      if (at < (uint32_t)count && atomicOr(&seen[at >> 5], bit) & bit) atomicOr(&twice[at >> 5], bit);
+    }
+  };
   int v = 0;
   for (; v + NT * E * U <= count; v += NT * E * U) {
     Vec<TS, E> x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) x[u] = load_vec<TS, E>(z + v + (u * NT + tid) * E);
-    if (v == 0) __syncthreads();  // (the listed logits are read before any is overwritten)
+    if (v == 0) claim();
 #pragma unroll
-    for (int u = 0; u < U; ++u) store_vec<TG, E>(g + v + (u * NT + tid) * E, gradient(x[u]));
+    for (int u = 0; u < U; ++u) store_vec<TG, E, STREAM>(g + v + (u * NT + tid) * E, gradient(x[u]));
   }
-  if (v == 0) __syncthreads();
+  if (v == 0) claim();
   for (v += tid * E; v < count; v += NT * E) {
     if (v + E <= count) {
-      store_vec<TG, E>(g + v, gradient(load_vec<TS, E>(z + v)));
+      store_vec<TG, E, STREAM>(g + v, gradient(load_vec<TS, E>(z + v)));
     } else {
       for (int e = v; e < count; ++e) g[e] = from_f32<TG>(some ? c * share((float)z[e]) : 0.f);
     }
   }
   __syncthreads();
+  if (!some) return;
+  for (int j = tid; j < a.top; j += NT) {
+    const int32_t id = ids[j];
+    const uint32_t at = place(id);
+    if (at >= (uint32_t)count) continue;
+    float p = parts[j];
+    if (twice[at >> 5] >> (at & 31) & 1) {
+      p = 0.f;
+      for (int i = 0; i < a.top; i += 8) {
+        typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+        const i32x4 lo = *(const i32x4 *)&ids[i], hi = *(const i32x4 *)&ids[i + 4];
+        uint32_t same = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (at[i] < 0) continue;
-    float p = 0.f;
-    for (int j = 0; j < a.top; ++j)
-      if (ids[j] == v0 + at[i]) p += parts[j];
-    g[at[i]] = from_f32<TG>(c * (share(zj[i]) - p));
+        for (int e = 0; e < 4; ++e) same |= (uint32_t)(lo[e] == id) << e | (uint32_t)(hi[e] == id) << (e + 4);
+        for (; same; same &= same - 1) p += parts[i + __ffs(same) - 1];
+      }
+    }
+    g[at] = from_f32<TG>(c * (share(listed[j]) - p));
   }
 }
 
 template <typename TS, typename TT>
 hipError_t distill_launch(const DistillArgs &a, hipStream_t stream) {
-  if (a.rows < 1024)
-    hipLaunchKernelGGL((k_distill<TS, TT, kDistillWide>), dim3((unsigned)a.rows), dim3(kDistillWide), 0,
-                       stream, a);
+  const dim3 grid((unsigned)a.rows);
+  if (a.vocab <= kDistillNarrow)
+    hipLaunchKernelGGL((k_distill<TS, TT, 64>), grid, dim3(64), 0, stream, a);
   else
-    hipLaunchKernelGGL((k_distill<TS, TT, kDistillThreads>), dim3((unsigned)a.rows),
-                       dim3(kDistillThreads), 0, stream, a);
+    hipLaunchKernelGGL((k_distill<TS, TT, kDistillThreads>), grid, dim3(kDistillThreads), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -242,12 +281,21 @@ hipError_t distill_as(const DistillArgs &a, int tt, hipStream_t stream) {
   return distill_launch<TS, f16_t>(a, stream);
 }
 
+template <typename TS, typename TT, typename TG, int NT, int S>
+hipError_t grad_slabs(const DistillArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.vocab + S - 1) / S * a.rows));
+  const size_t lds = (a.top + 7) / 8 * 8 * 3 * sizeof(int32_t);
+  const bool big = a.rows * a.vocab * (int64_t)sizeof(TG) >= kStreamBytes;
+  if (big)
+    hipLaunchKernelGGL((k_distill_grad<TS, TT, TG, NT, S, true>), grid, dim3(NT), lds, stream, a);
+  else
+    hipLaunchKernelGGL((k_distill_grad<TS, TT, TG, NT, S, false>), grid, dim3(NT), lds, stream, a);
+  return hipGetLastError();
+}
 template <typename TS, typename TT, typename TG>
 hipError_t grad_launch(const DistillArgs &a, hipStream_t stream) {
-  const int64_t groups = (a.vocab + kDistillSlab - 1) / kDistillSlab * a.rows;
-  hipLaunchKernelGGL((k_distill_grad<TS, TT, TG>), dim3((unsigned)groups), dim3(kDistillThreads), 0,
-                     stream, a);
-  return hipGetLastError();
+  return a.vocab <= kDistillNarrow ? grad_slabs<TS, TT, TG, 64, kDistillNarrow>(a, stream)
+                                   : grad_slabs<TS, TT, TG, kDistillThreads, kDistillSlab>(a, stream);
 }
 template <typename TS, typename TT>
 hipError_t grad_from(const DistillArgs &a, int gt, hipStream_t stream) {

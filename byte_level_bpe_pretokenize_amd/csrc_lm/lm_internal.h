@@ -8,6 +8,12 @@
 
 #include "../../include/bpe_lm.h"
 
+#if defined(__HIPCC__)
+#define BPE_HD __host__ __device__ __forceinline__
+#else
+#define BPE_HD inline
+#endif
+
 namespace bpe {
 
 // Whether that many workgroups of so many threads are one launch (of fewer than
@@ -180,12 +186,6 @@ bool cache_tokens_ok(const bpe_cache &c, int64_t n, int64_t token_stride, int64_
 void cache_shape(CacheArgs *a, bool write);
 inline int64_t cache_workgroups(const CacheArgs &a) { return (a.n + a.tokens - 1) / a.tokens; }
 
-#if defined(__HIPCC__)
-#define BPE_HD __host__ __device__ __forceinline__
-#else
-#define BPE_HD inline
-#endif
-
 // The slot of position p of a request whose blocks are row[0 .. width), or -1
 // where it is read as zeros; *status gets why.
 BPE_HD int64_t cache_slot(const int32_t *row, int64_t width, int32_t bs, int64_t n_slots,
@@ -250,7 +250,10 @@ hipError_t launch_verify(const VerifyArgs &a, int type, hipStream_t stream);
 // ---- distillation -------------------------------------------------------------------
 constexpr int kDistillSlab = 8192;    // logits per workgroup of the gradient
 constexpr int kDistillThreads = 256;
-constexpr int kDistillWide = 1024;    // threads of the loss's widest workgroup
+// Logits up to which one wave takes a row instead of kDistillThreads: 16,000 rows of
+// 876 bfloat16 logits 19 us instead of 47 (the loss) and 19 instead of 30 (the
+// gradient), 8,000 of 2,000 15 instead of 27.
+constexpr int kDistillNarrow = 2048;
 
 struct DistillArgs {
   const void *student, *teacher;

@@ -354,7 +354,7 @@ int bpe_verify_drafts(const void *d_target, int prob_type, int64_t n_rows, int64
  * all -infinity, has loss 0 and a gradient of zeros.  A term with P_k = 0 is 0;
  * a listed token with P_k > 0 whose z is -infinity makes the loss infinite.
  * 2^-20 <= temperature <= 2^20, 0 <= top <= BPE_MAX_TOP, 1 <= vocab <= BPE_MAX_ROWS,
- * n_rows < 2^22.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
+ * n_rows < 2^24.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */
 int bpe_distill(const void *d_student, int student_type, int64_t n_rows, int64_t vocab,
                 int64_t student_stride, const int32_t *d_ids, int64_t ids_stride,

@@ -49,9 +49,10 @@ def test_temperatures(T):
     check_distill(*rows(20, 3001, 40, BF16, F32, 4), T, F32)
 
 
-@pytest.mark.parametrize("N", [1023, 1024, 1500])
-def test_rows_on_both_sides_of_the_variants(N):
-    check_distill(*rows(N, 600, 9, BF16, F32, 5), 1.5)
+@pytest.mark.parametrize("V", [2040, 2047, 2048, 2049, 2060])
+def test_both_sides_of_the_variants(V):
+    check_distill(*rows(300, V, 9, BF16, F32, 5), 1.5)
+    check_distill(*rows(30, V, 200, F32, BF16, 6), 0.8)
 
 
 @pytest.mark.parametrize("K", [0, 255, 256, 257, 1024])

@@ -124,7 +124,7 @@ def grad_rc(student=P, st=1, N=9, V=100, ss=100, ids=P, is_=5, teacher=P, tt=0, 
 
 
 BAD_ROWS = [dict(student=None), dict(ids=None), dict(teacher=None), dict(status=None), dict(st=3), dict(tt=-1),
-            dict(N=-1), dict(N=1 << 22), dict(V=0), dict(V=_lib.MAX_ROWS + 1, ss=1 << 28), dict(ss=99),
+            dict(N=-1), dict(N=1 << 24), dict(V=0), dict(V=_lib.MAX_ROWS + 1, ss=1 << 28), dict(ss=99),
             dict(is_=4), dict(ts=4), dict(K=1025, is_=2000, ts=2000), dict(K=-1), dict(T=0.0), dict(T=-1.0),
             dict(T=float("nan")), dict(T=float("inf")), dict(T=2.0 ** -21), dict(T=2.0 ** 21), dict(stats=None)]
 
