@@ -13,6 +13,13 @@ tokens are decoded.
 
 Training: next-token cross entropy of the same stand-in on the encoded text,
 with lm.embedding's gradient for the table.
+
+Drafting: the same serving with a small drafter (a table: the last token alone
+gives the next one's logits) that proposes several tokens a step.  The cache is
+held in 8 bits (lm.cache_write, lm.cache_read), the target looks at all proposed
+tokens at once, and lm.verify_drafts says which of them stand and draws the one
+after them; what does not stand leaves the cache.  The drafter learns from the
+target's top logits (lm.distillation).
 """
 from __future__ import annotations
 
@@ -124,8 +131,124 @@ def train(model, special, weight, texts, steps: int = 10, rate: float = 0.1):
     return losses
 
 
+def contexts(cache, table, lengths, dim: int, status):
+    """Each request's tokens in the cache, one after another, and where they start."""
+    codes, scales, group = cache
+    off = torch.zeros(lengths.numel() + 1, dtype=torch.int64, device=lengths.device)
+    torch.cumsum(lengths, 0, out=off[1:])
+    return lm.cache_read(codes, scales, group, table, BLOCK, off, int(off[-1]), dim=dim,
+                         out_dtype=torch.float32, status=status), off
+
+
+def draw(logits, sample, status):
+    """One token per row, from uniform numbers: a request of one row has no draft."""
+    n = logits.shape[0]
+    p = torch.softmax(logits, 1)
+    tokens, _ = lm.verify_drafts(p, torch.zeros(n, dtype=torch.int32, device=p.device),
+                                 torch.arange(n + 1, device=p.device), torch.zeros_like(sample), sample,
+                                 status=status)
+    return tokens, p
+
+
+def serve_drafts(model, special, weight, drafter, texts, steps: int = 6, k: int = 3, heads: int = 4,
+                 seed: int = 0, held: torch.dtype = torch.int8):
+    """The texts continued by `steps` steps of up to k + 1 tokens: the IDs that each
+    request got in each step, and each step's drafts (R, k) and uniform numbers
+    (theirs (k, R), accept (R, k + 1), sample (R))."""
+    dev, (V, D), R = model.device, weight.shape, len(texts)
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    ids, id_off = model.encode_batch_special(*batch(model, texts), bos_id=special["bos"])
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    size = (id_off[1:] - id_off[:-1]).to(torch.int32)
+    width = (int(size.max()) + steps * (k + 1)) // BLOCK + 1
+    free = torch.randperm(R * width, device=dev).to(torch.int32)
+    cache = lm.empty_cache(R * width * BLOCK, heads, D // heads, held, device=dev)
+    table = torch.full((R, width), -1, dtype=torch.int32, device=dev)
+    mask, at = letters_mask(model, V), torch.arange(width, device=dev)
+    mask_row = torch.zeros(R * (k + 1), dtype=torch.int32, device=dev)
+
+    def place(new, new_off, cached):
+        """New tokens into the cache; the contexts' lengths, and the blocks left."""
+        slots, _, lengths, used = lm.block_tables(new_off, new.numel(), cached, free, table, BLOCK, status=status)
+        x = lm.embed(weight, new, D ** 0.5, status=status)
+        lm.cache_write(x.view(-1, heads, D // heads), slots, *cache, status=status)
+        return lengths, free[int(used):]
+
+    # all of a prompt but its last token, which the first step looks at with its drafts
+    last = ids[id_off[1:] - 1].clone()
+    keep = torch.ones(ids.numel(), dtype=torch.bool, device=dev)
+    keep[id_off[1:] - 1] = False
+    lengths, free = place(ids[keep], id_off - torch.arange(R + 1, device=dev), torch.zeros_like(size))
+    rows_off = torch.arange(R + 1, device=dev) * (k + 1)
+    got, numbers = [[] for _ in range(R)], []
+    for _ in range(steps):
+        u = torch.rand(k, R, device=dev, generator=gen)
+        accept = torch.rand(R, k + 1, device=dev, generator=gen)
+        sample = torch.rand(R, device=dev, generator=gen)
+        # the drafter: k tokens one by one, and the probabilities they were drawn from
+        new, q = [last], torch.zeros(R, k + 1, V, device=dev)
+        for i in range(k):
+            logits = lm.process_logits(lm.embed(drafter, new[-1], status=status) @ weight.t(), mask=mask,
+                                       mask_row=mask_row[:R], status=status)
+            token, q[:, i] = draw(logits, u[i], status)
+            new.append(token)
+        new = torch.stack(new, 1)
+        numbers.append((new[:, 1:], u, accept, sample))
+        before = lengths
+        lengths, free = place(new.view(-1), rows_off, before)
+        # the target: at each new token the average of what came up to it
+        x, off = contexts(cache, table, lengths, D // heads, status)
+        total = torch.cumsum(x.view(-1, D).double(), 0)
+        total = torch.cat((torch.zeros_like(total[:1]), total))
+        here = (before[:, None] + torch.arange(1, k + 2, device=dev)).long()
+        hidden = ((total[off[:-1, None] + here] - total[off[:-1, None]]) / here[:, :, None]).float()
+        logits = lm.process_logits(hidden.view(-1, D) @ weight.t(), mask=mask, mask_row=mask_row, status=status)
+        drafted = torch.cat((new[:, 1:], torch.full_like(new[:, :1], -1)), 1)
+        tokens, counts = lm.verify_drafts(torch.softmax(logits, 1), drafted.reshape(-1), rows_off, accept.view(-1),
+                                          sample, draft=q.view(-1, V), status=status)
+        tokens = tokens.view(R, k + 1)
+        last = tokens.gather(1, counts.long()[:, None] - 1)[:, 0]
+        # what does not stand leaves the cache: its blocks are free again
+        want, lengths = (lengths + BLOCK - 1) // BLOCK, before + counts
+        back = (at >= ((lengths + BLOCK - 1) // BLOCK)[:, None]) & (at < want[:, None])
+        free = torch.cat((table[back], free))
+        for r, (row, n) in enumerate(zip(tokens.tolist(), counts.tolist())):
+            got[r].append(row[:n])
+    if int(status):
+        raise RuntimeError(f"device status {int(status):#x}")
+    return got, numbers
+
+
+def train_drafter(model, special, weight, texts, steps: int = 10, rate: float = 0.1, top: int = 16,
+                  temperature: float = 2.0, drafter=None):
+    """A drafter from the target's top logits on the texts: (drafter, losses)."""
+    ids, id_off = model.encode_batch_special(*batch(model, texts), bos_id=special["bos"])
+    status = torch.zeros(1, dtype=torch.int32, device=model.device)
+    x = torch.cumsum(lm.embed(weight, ids, weight.shape[1] ** 0.5, status=status).double(), 0)
+    first = torch.repeat_interleave(id_off[:-1], id_off.diff(), output_size=ids.numel())
+    at = torch.arange(ids.numel(), device=model.device)
+    x = (x - torch.where(first[:, None] > 0, x[first - 1], torch.zeros_like(x))) / (at - first + 1)[:, None]
+    best = (x.float() @ weight.t()).topk(top, 1)
+    w = (torch.zeros_like(weight) if drafter is None else drafter.clone()).requires_grad_()
+    losses = []
+    for _ in range(steps):
+        logits = lm.embedding(w, ids, status=status) @ weight.t()
+        loss = lm.distillation(logits, best.indices.to(torch.int32), best.values, temperature, status=status).mean()
+        (g,) = torch.autograd.grad(loss, w)
+        with torch.no_grad():
+            w -= rate * weight.shape[0] * g
+        losses.append(float(loss.detach()))
+    if int(status):
+        raise RuntimeError(f"device status {int(status):#x}")
+    return w.detach(), losses
+
+
 if __name__ == "__main__":
     m, sp, table = load()
     for text, more in zip(TEXTS, serve(m, sp, table, TEXTS)[0]):
         print(f"{text!r} -> {more!r}")
     print("losses:", " ".join(f"{x:.3f}" for x in train(m, sp, table, TEXTS * 20)))
+    small, fell = train_drafter(m, sp, table, TEXTS * 20)
+    print("drafter's losses:", " ".join(f"{x:.3f}" for x in fell))
+    drafted = serve_drafts(m, sp, table, small, TEXTS)[0]
+    print("tokens a step with drafts:", " ".join(f"{sum(map(len, x)) / len(x):.1f}" for x in drafted))
