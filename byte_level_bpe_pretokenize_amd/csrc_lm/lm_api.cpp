@@ -244,7 +244,7 @@ int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t
   a.x = d_x;
   a.slots = d_slots;
   cache_shape(&a, true);
-  if (!launch_fits(cache_workgroups(a), kCacheThreads)) return BPE_EINVAL;
+  if (!cache_fits(a)) return BPE_EINVAL;
   return launch_cache_write(a, x_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }
 
@@ -275,7 +275,7 @@ int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_req
   a.stride = table_stride;
   a.bs = divisor(block_size);
   cache_shape(&a, false);
-  if (!launch_fits(cache_workgroups(a), kCacheThreads)) return BPE_EINVAL;
+  if (!cache_fits(a)) return BPE_EINVAL;
   return launch_cache_read(a, out_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }
 

@@ -184,6 +184,7 @@ int32_t cache_row_bytes(const bpe_cache &c);
 bool cache_ok(const bpe_cache &c);
 bool cache_tokens_ok(const bpe_cache &c, int64_t n, int64_t token_stride, int64_t head_stride);
 void cache_shape(CacheArgs *a, bool write);
+bool cache_fits(const CacheArgs &a);  // (shaped)
 inline int64_t cache_workgroups(const CacheArgs &a) { return (a.n + a.tokens - 1) / a.tokens; }
 
 // The slot of position p of a request whose blocks are row[0 .. width), or -1

@@ -133,7 +133,7 @@ bool cache_ok(const bpe_cache &c) {
 // Strides of tokens and heads: token by token or head by head, without overlap.
 bool cache_tokens_ok(const bpe_cache &c, int64_t n, int64_t token_stride, int64_t head_stride) {
   const int64_t most = (int64_t)1 << 32;
-  if (n < 0 || n > BPE_MAX_IDS || n * c.heads >= most) return false;
+  if (n < 0 || n > BPE_MAX_IDS - kCacheTokens) return false;
   const bool many = n > 1, heads = c.heads > 1;
   if ((many && (token_stride < c.dim || token_stride > most)) ||
       (heads && (head_stride < c.dim || head_stride > most)))
@@ -183,6 +183,12 @@ int32_t verify_tiles(int64_t vocab) {
 int64_t verify_workgroups(int64_t n_requests, int64_t vocab) {
   const int64_t per = kVerifyThreads / 16;
   return n_requests * ((verify_regions(vocab) + per - 1) / per);
+}
+
+// Whether a cache's tokens are one launch (which the header's bound on lanes is
+// stricter than).
+bool cache_fits(const CacheArgs &a) {
+  return a.n * a.per_token.d < (int64_t)1 << 33 && launch_fits(cache_workgroups(a), kCacheThreads);
 }
 
 // Whether the gradient is one launch.

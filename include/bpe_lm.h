@@ -259,7 +259,8 @@ typedef struct {
  * -127, 448 and -448, 15 and 0), NaN gets code 0, and a group without a finite
  * element has scale (and lowest value) 0.  BPE_UINT4 takes magnitudes above
  * 2^126 as 2^126, so that a group's width stays finite.
- * n * heads < 2^32.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
+ * n <= 2^30 - 64, n * heads * ceil(dim / group) * group < 2^36.
+ * Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */
 int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t n,
                     int64_t token_stride, int64_t head_stride, const int64_t *d_slots,
@@ -269,8 +270,8 @@ int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t
  * Reads the requests' tokens back, packed: for t in [off[r], off[r + 1])
  *   out[t] = the values of slot table[r][p / block_size] * block_size + p % block_size,
  *   p = start[r] + t - off[r]
- * each a float32 rounded once to out_type (BPE_UINT4: code * scale + lowest
- * with one rounding).
+ * formed in float32, with at most one rounding there, and rounded once to
+ * out_type.
  *  d_off    int64 [n_requests + 1]: increasing, within [0, n]; offsets that are
  *           not set BPE_STATUS_BAD_ID_OFFSETS, and which tokens are read is
  *           open.  Rows of out outside [off[0], off[n_requests]) are left as
@@ -284,7 +285,7 @@ int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t
  *           (BPE_STATUS_TABLE_FULL), past slot n_slots (BPE_STATUS_BAD_SLOT) and
  *           past position INT32_MAX (BPE_STATUS_BAD_LENGTH).
  *  d_out    [n][heads][dim] of out_type, strides as those of d_x.
- * n <= 2^30, n * heads < 2^32, n_requests <= 2^30.
+ * n <= 2^30 - 64, n * heads * ceil(dim / 8) < 2^33, n_requests <= 2^30.
  * Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */
 int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_requests,
@@ -311,6 +312,7 @@ size_t bpe_verify_drafts_workspace_bytes(int64_t n_requests, int64_t vocab);
  * Comparisons and sums are in 64 bits.  A request of one row has no draft.
  *  tokens   int32 [n_rows]: in a request's rows its drafts that stand, the next
  *           token, then -1.  Rows that are no request's are left as they were.
+ *           May be draft_ids itself.  Requests' rows must not overlap.
  *  counts   int32 [n_requests]: how many tokens it got (0 without rows).
  *  d_target, d_draft   [n_rows][vocab] of prob_type, rows target_stride and
  *           draft_stride apart.  Rows need not add up to 1.  Negative entries,

@@ -99,11 +99,35 @@ static void refusals() {
   CHECK(!cache_tokens_ok(good, -1, 2048, 128) && !cache_tokens_ok(good, 5, 2048, 127));
   CHECK(cache_tokens_ok(good, 5, G, 128) && !cache_tokens_ok(good, 5, G + 1, 128));
   CHECK(!cache_tokens_ok(good, 1, 0, G + 1));
-  CHECK(cache_tokens_ok(good, G / 16 - 1, 2048, 128) && !cache_tokens_ok(good, G / 16, 2048, 128));
   bpe_cache one = good;
   one.heads = 1;
-  CHECK(cache_tokens_ok(one, 5, 128, 0) && cache_tokens_ok(one, BPE_MAX_IDS, 128, -7));
-  CHECK(!cache_tokens_ok(one, BPE_MAX_IDS + 1, 128, 0));
+  CHECK(cache_tokens_ok(one, 5, 128, 0) && cache_tokens_ok(one, BPE_MAX_IDS - 64, 128, -7));
+  CHECK(!cache_tokens_ok(one, BPE_MAX_IDS - 63, 128, 0));
+}
+
+// The launch of the tokens that pass the checks has fewer than 2^32 threads, and the
+// header's bound is the one that is checked.
+static void limit() {
+  int fits = 0, not_ = 0;
+  for (int i = 0; i < 200000; ++i) {
+    CacheArgs a = {};
+    a.c.heads = i % 3 ? 1 + (int)below(16) : 1 + (int)below(BPE_MAX_HEADS);
+    a.c.dim = i % 5 ? 1 + (int)below(BPE_MAX_DIM) : 1 + (int)below(40);
+    a.c.group = kCacheMinGroup << below(6);
+    const bool write = i % 2;
+    cache_shape(&a, write);
+    const int64_t most = BPE_MAX_IDS - kCacheTokens;
+    a.n = i % 7 ? std::min(most, ((int64_t)1 << 33) / a.per_token.d + below(5) - 2) : 1 + below(most);
+    const int64_t per = write ? (int64_t)a.groups * a.c.group / 8 : (a.c.dim + 7) / 8;
+    CHECK(cache_fits(a) == (a.n * a.c.heads * per < (int64_t)1 << 33));
+    if (!cache_fits(a)) {
+      ++not_;
+      continue;
+    }
+    ++fits;
+    CHECK(cache_workgroups(a) * a.tokens >= a.n && cache_workgroups(a) * kCacheThreads < (int64_t)1 << 32);
+  }
+  CHECK(fits > 1000 && not_ > 1000);
 }
 
 // The request of a token, with empty requests, and in range for offsets of any
@@ -192,7 +216,7 @@ static void regions() {
 
 int main(int argc, char **argv) {
   const std::pair<const char *, void (*)()> checks[] = {
-      {"shape", shape}, {"refusals", refusals}, {"request", request}, {"slot", slot}, {"gradient", gradient}, {"regions", regions}};
+      {"shape", shape}, {"refusals", refusals}, {"limit", limit}, {"request", request}, {"slot", slot}, {"gradient", gradient}, {"regions", regions}};
   for (const auto &c : checks)
     if (argc == 2 && !strcmp(argv[1], c.first)) {
       c.second();

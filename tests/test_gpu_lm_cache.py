@@ -10,7 +10,7 @@ from lm_reference import check, f64
 from byte_level_bpe_pretokenize_amd import _lib, lm
 
 from gpu_util import device
-from test_gpu_lm import BF16, F16, F32, dev, gen, randn, status
+from test_gpu_lm import BF16, F16, F32, dev, gen, randn, status, strided
 
 pytestmark = pytest.mark.gpu
 
@@ -236,6 +236,18 @@ def test_read_bad_pages(kind):
     check_read(c, s, 32, np.zeros((3, 0), np.int32), bs, off, 120, D, kind, F32, bits=_lib.STATUS_TABLE_FULL)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_read_by_a_strided_table_from_a_strided_cache(kind):
+    lengths, bs, H, D, group = [50, 20, 90, 16], 16, 3, 40, 16
+    table, n_slots = paged(lengths, bs)
+    parts = [cache_of(n_slots, H, D, kind, group, k) for k in range(2)]
+    c = torch.stack([x.view(torch.uint8) for x, _ in parts], 1)[:, 1].view(KINDS[kind])
+    s = torch.stack([x for _, x in parts], 1)[:, 1]
+    assert not c.is_contiguous() and not s.is_contiguous()
+    off = np.concatenate([[0], np.cumsum(lengths)])
+    check_read(c, s, group, table, bs, off, int(off[-1]), D, kind, F16, tab=strided(dev(table), 3))
+
+
 def test_read_bad_offsets():
     lengths, bs = [40, 40, 40], 8
     table, n_slots = paged(lengths, bs)
@@ -351,6 +363,25 @@ def test_another_stream_outlives_its_inputs():
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got, want) and int(st.item()) == 0
     del noise
+
+
+def test_scales_of_any_value():
+    """What a caller puts into the scales is multiplied as it is."""
+    c, s = cache_of(8, 1, 16, "int8", 16)
+    c.view(torch.uint8).copy_(torch.arange(128, dtype=torch.uint8, device=device()).view(8, 1, 16) * 2)
+    big = torch.finfo(F32).max
+    s.copy_(torch.tensor([big / 127, -1.0, float("inf"), float("nan"), 0.0, 2.0 ** -140, big, -big],
+                         device=device()).view(8, 1, 1))
+    table, off = dev(np.zeros((1, 1), np.int32)), dev(np.array([0, 8]))
+    got = lm.cache_read(c, s, 16, table, 8, off, 8, out_dtype=F32)
+    want = c.float() * s
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+def test_inference_tensors_are_taken():
+    with torch.inference_mode():
+        c, s = cache_of(8, 1, 16, "e4m3", 16)
+        lm.cache_write(tokens_of(2, 1, 16, F32, 1), dev(np.arange(2)), c, s, 16)
 
 
 def test_writes_count_as_modified():

@@ -207,6 +207,21 @@ def test_a_large_vocabulary():
         assert counts.tolist() == [1] and got.tolist() == [want, -1]
 
 
+@pytest.mark.parametrize("V", [900, 70000])
+@pytest.mark.parametrize("with_draft", [True, False])
+def test_in_place(V, with_draft):
+    p, q, ids, off, accept, sample = batch([4, 1, 0, 70, 7] * 3, V, F32 if V < 1000 else BF16, 2, with_draft)
+    want = lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q)
+    got = lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q, tokens=ids)
+    assert got[0] is ids and torch.equal(ids, want[0]) and torch.equal(got[1], want[1])
+
+
+def test_inference_tensors_are_taken():
+    with torch.inference_mode():
+        p, q, ids, off, accept, sample = batch([4, 1], 100, F32, 2)
+        lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q, tokens=ids)
+
+
 def test_a_workspace_of_ones_own():
     p, q, ids, off, accept, sample = batch([4, 1, 0, 7], 70000, BF16, 2)
     want = lm.verify_drafts(p, ids, dev(off), accept, sample, draft=q)

@@ -27,7 +27,7 @@ def driver(tmp_path_factory):
     return str(exe)
 
 
-@pytest.mark.parametrize("check", ["shape", "refusals", "request", "slot", "gradient", "regions"])
+@pytest.mark.parametrize("check", ["shape", "refusals", "limit", "request", "slot", "gradient", "regions"])
 def test_layout(driver, check):
     env = dict(os.environ, ASAN_OPTIONS="detect_leaks=1:abort_on_error=1:verify_asan_link_order=0",
                UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
