@@ -202,16 +202,31 @@ __device__ __forceinline__ int64_t first_past(F get, int n, int64_t i0, double s
 template <typename T, bool DRAFT, typename F>
 __device__ __forceinline__ int32_t draw(const VerifyArgs &a, const Row<T, DRAFT> &row, bool less, float u, F sum) {
   const int lane = lane_id(), per = (a.regions + 63) / 64;
+  // a lane's regions are consecutive; those of up to 131,072 tokens are loaded
+  // together and kept
+  constexpr int KEPT = 4;
+  double kept[KEPT];
+#pragma unroll
+  for (int i = 0; i < KEPT; ++i) {
+    const int g = lane * per + i;
+    kept[i] = i < per && g < a.regions ? sum(g) : 0.0;
+  }
   auto mine = [&](int i) { return lane * per + i < a.regions ? sum(lane * per + i) : 0.0; };
   double total = 0.0;
-  for (int i = 0; i < per; ++i) total += mine(i);
+  if (per <= KEPT) {
+#pragma unroll
+    for (int i = 0; i < KEPT; ++i) total += kept[i];
+  } else {
+    for (int i = 0; i < per; ++i) total += mine(i);
+  }
   total = lane_f64(wave_scan(total), 63);
   if (!(total > 0.0)) return -1;
   // (past the upper end, NaN included, the last token of positive weight)
   const double share = u < 1.f ? fmax((double)u, 0.0) * total : total;
   double before = 0.0;
   int64_t g_last = 0, last = -1;
-  int64_t g = first_past(mine, per, lane * per, share, &before, &g_last);
+  int64_t g = per <= KEPT ? first_past([&](int i) { return kept[i]; }, KEPT, lane * per, share, &before, &g_last)
+                          : first_past(mine, per, lane * per, share, &before, &g_last);
   if (g < 0) {
     g = g_last;
     before = -INFINITY;  // its last token of positive weight

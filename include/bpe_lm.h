@@ -312,7 +312,7 @@ size_t bpe_verify_drafts_workspace_bytes(int64_t n_requests, int64_t vocab);
  * Comparisons and sums are in 64 bits.  A request of one row has no draft.
  *  tokens   int32 [n_rows]: in a request's rows its drafts that stand, the next
  *           token, then -1.  Rows that are no request's are left as they were.
- *           May be draft_ids itself.  Requests' rows must not overlap.
+ *           May be draft_ids itself.
  *  counts   int32 [n_requests]: how many tokens it got (0 without rows).
  *  d_target, d_draft   [n_rows][vocab] of prob_type, rows target_stride and
  *           draft_stride apart.  Rows need not add up to 1.  Negative entries,
