@@ -69,6 +69,11 @@ __device__ __forceinline__ Entry load_entry(const DistillArgs &a, int64_t n, int
 
 // A workgroup per row: one pass over the logits with a running maximum and sum
 // per thread, joined over the workgroup; the listed logits are gathered before.
+// 4,096 rows of 128,256 bfloat16 logits, 1.05 GB, take 182 us, 5.8 TB/s, bound by
+// memory (an exponential per logit keeps the vector units about half busy).  Few
+// rows are bound by what one CU reads: 48 rows of 32,256 6.6 us, one of 128,256 12.5
+// (workgroups of 1,024 threads were no faster from 1 to 1,500 rows, and slower for
+// many).
 // With e_j = exp((t_j - largest t) / T), the loss is
 //   T^2 (sum e_j ((t_j - largest t) - (z_j - largest z)) / (T sum e_j) + log sum z - log sum t)
 // whose last terms and sum are in 64 bits: it is the difference of values larger
@@ -173,7 +178,10 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
 // logit they would cost more.)  A token that is listed twice gets the same value
 // from both entries: each adds up all of the token's, in their order.  Which ones
 // are is known from two bits for each of the slab's logits: listed, and listed by
-// another entry too.
+// another entry too (adding up over the list for every entry took 118 us instead of
+// 28 for 16,000 rows of 876 with lists of 200).  4,096 rows of 128,256 bfloat16
+// logits, 2.1 GB, take 380 us, 5.5 TB/s, bound by memory; with the table as a word
+// per logit, 32 KB of LDS more, 418.
 template <typename TS, typename TT, typename TG, int NT, int S, bool STREAM>
 __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   constexpr int E = sizeof(TS) == 2 && sizeof(TG) == 2 ? 8 : 4;
