@@ -70,13 +70,13 @@ __device__ __forceinline__ Entry load_entry(const DistillArgs &a, int64_t n, int
 // A workgroup per row: one pass over the logits with a running maximum and sum
 // per thread, joined over the workgroup; the listed logits are gathered before.
 // 4,096 rows of 128,256 bfloat16 logits, 1.05 GB, take 182 us, 5.8 TB/s, bound by
-// memory (an exponential per logit keeps the vector units about half busy).  Few
+// memory (the vector instructions alone would take about two thirds of that).  Few
 // rows are bound by what one CU reads: 48 rows of 32,256 6.6 us, one of 128,256 12.5
 // (workgroups of 1,024 threads were no faster from 1 to 1,500 rows, and slower for
 // many).
 // With e_j = exp((t_j - largest t) / T), the loss is
-//   T^2 (sum e_j ((t_j - largest t) - (z_j - largest z)) / (T sum e_j) + log sum z - log sum t)
-// whose last terms and sum are in 64 bits: it is the difference of values larger
+//   T^2 (sum e_j ((t_j - largest t) - (z_j - largest z)) / (T sum e_j) + log (sum z / sum t))
+// whose logarithm and sum are in 64 bits: it is the difference of values larger
 // than itself where the student is near the teacher.
 template <typename TS, typename TT, int NT>
 __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     }
     const bool some = x.s != 0.f && t.s != 0.f;
     const double T = a.temperature;
-    a.losses[n] = some ? (float)(T * T * (sum * by / t.s + log((double)x.s) - log((double)t.s))) : 0.f;
+    a.losses[n] = some ? (float)(T * T * (sum * by / t.s + log((double)x.s / t.s))) : 0.f;
     float *o = a.stats + n * 4;
     o[0] = x.m;
     o[1] = x.s;

@@ -251,9 +251,11 @@ hipError_t launch_verify(const VerifyArgs &a, int type, hipStream_t stream);
 // ---- distillation -------------------------------------------------------------------
 constexpr int kDistillSlab = 8192;    // logits per workgroup of the gradient
 constexpr int kDistillThreads = 256;
-// Logits up to which one wave takes a row instead of kDistillThreads: 16,000 rows of
-// 876 bfloat16 logits 19 us instead of 47 (the loss) and 19 instead of 30 (the
-// gradient), 8,000 of 2,000 15 instead of 27.
+// Logits up to which one wave takes a row instead of kDistillThreads.  Loss and
+// gradient in us, one wave (256 threads): 16,000 rows of 876 bfloat16 logits with
+// lists of 16 18 and 18 (40 and 34), 8,000 of 2,048 12 and 14 (24 and 18), 100 of 768
+// 4.9 and 4.8 (5.2 and 4.5); behind only for the gradient of float32 rows with long
+// lists (16,000 of 876, lists of 200: 45 and 34).
 constexpr int kDistillNarrow = 2048;
 
 struct DistillArgs {
