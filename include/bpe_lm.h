@@ -17,10 +17,10 @@
  *    bpe_distill_grad
  *
  * Conventions, next to those of bpe.h:
- *  - Every d_* pointer (and every pointer inside bpe_logits_args) is device
- *    memory on the current device.  Nothing is allocated and the host is
- *    never synchronized; every call is kernel launches on `hip_stream` only,
- *    so it can be captured into a graph.
+ *  - Every d_* pointer (and every pointer inside bpe_logits_args and
+ *    bpe_cache) is device memory on the current device.  Nothing is allocated
+ *    and the host is never synchronized; every call is kernel launches on
+ *    `hip_stream` only, so it can be captured into a graph.
  *  - Host-checkable problems return a negative BPE_E* code and enqueue
  *    nothing.  A count of zero is no problem.
  *  - *d_status (int32, device) receives BPE_STATUS_* bits for what only the
@@ -34,7 +34,7 @@
  *    element.
  *  - Sums and products are formed in float32 and rounded once, to nearest
  *    even, on the way out.  Results do not depend on scheduling: the same
- *    inputs give the same bits.
+ *    inputs give the same bits (but for what is called open below).
  */
 #ifndef BPE_LM_H
 #define BPE_LM_H
@@ -353,8 +353,9 @@ int bpe_verify_drafts(const void *d_target, int prob_type, int64_t n_rows, int64
  * ID -1 is an entry that holds no token; other IDs outside [0, vocab) set
  * BPE_STATUS_BAD_ID and count as that.  A token that is listed twice counts with
  * both entries.  A row that lists no token above -infinity, or whose logits are
- * all -infinity, has loss 0 and a gradient of zeros.  A term with P_k = 0 is 0;
- * a listed token with P_k > 0 whose z is -infinity makes the loss infinite.
+ * all -infinity, has loss 0 and a gradient of zeros.  A term with P_k = 0 is 0,
+ * and a P_k below 2^-126 of the largest counts as that; a listed token with another
+ * P_k whose z is -infinity makes the loss infinite.
  * 2^-20 <= temperature <= 2^20, 0 <= top <= BPE_MAX_TOP, 1 <= vocab <= BPE_MAX_ROWS,
  * n_rows < 2^24.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */

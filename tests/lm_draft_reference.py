@@ -181,6 +181,7 @@ def distill(z, ids, t, T, dloss=None):
             y, at, x = z[n] / T, ids[n, on], t[n, on] / T
             zm, ze, zs = _softmax(y)
             tm, te, ts = _softmax(x)
+            te[te < 2.0 ** -126] = 0.0  # (which float32 does not hold)
             q, P = ze / zs, te / ts
             sum_z = (9 * run + 40) * U
             sum_t = (9 * 8 + 40) * U

@@ -106,6 +106,16 @@ def test_masks():
     assert bool((lm.distill_grad(z, dev(ids), t, st, dl, 1.3)[[2, 5, 7]] == 0).all())
 
 
+def test_a_probability_that_float32_does_not_hold():
+    """A listed token 200 below the largest weighs nothing, also where the student's
+    logit is -infinity."""
+    z, ids, t = rows(4, 3000, 6, F32, F32, 20)
+    t[:, 2] = t.amax(1) - 200.0
+    z[torch.arange(4, device=device()), dev(ids)[:, 2].long()] = -float("inf")
+    losses, _, grad = check_distill(z, ids, t, 1.0)
+    assert bool(torch.isfinite(losses).all()) and bool(torch.isfinite(grad).all())
+
+
 def test_nan_and_infinity_spread_over_their_row():
     z, ids, t = rows(8, 900, 10, F32, F32, 10)
     z[1, 3] = float("nan")
