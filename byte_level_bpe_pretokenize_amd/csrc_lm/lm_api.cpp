@@ -346,11 +346,12 @@ int bpe_distill(const void *d_student, int student_type, int64_t n_rows, int64_t
   a.ids = d_ids;
   a.i_stride = ids_stride;
   a.top = (int32_t)top;
+  a.t_type = teacher_type;
   a.temperature = temperature;
   a.losses = d_losses;
   a.stats = d_stats;
   a.status = d_status;
-  return launch_distill(a, student_type, teacher_type, (hipStream_t)hip_stream) == hipSuccess
+  return launch_distill(a, student_type, (hipStream_t)hip_stream) == hipSuccess
              ? BPE_OK
              : BPE_EHIP;
 }
@@ -379,13 +380,14 @@ int bpe_distill_grad(const void *d_student, int student_type, int64_t n_rows, in
   a.ids = d_ids;
   a.i_stride = ids_stride;
   a.top = (int32_t)top;
+  a.t_type = teacher_type;
   a.temperature = temperature;
   a.in_stats = d_stats;
   a.dloss = d_dloss;
   a.grad = d_grad;
   a.g_stride = grad_stride;
   a.status = d_status;
-  return launch_distill_grad(a, student_type, teacher_type, grad_type, (hipStream_t)hip_stream) == hipSuccess
+  return launch_distill_grad(a, student_type, grad_type, (hipStream_t)hip_stream) == hipSuccess
              ? BPE_OK
              : BPE_EHIP;
 }

@@ -57,12 +57,16 @@ struct Entry {
   int32_t id;
   float t;
 };
-template <typename TT>
+// (The teacher's type is a branch: lists are short, and a kernel for each type would
+// be three times the code.)
 __device__ __forceinline__ Entry load_entry(const DistillArgs &a, int64_t n, int j) {
   Entry x = {-1, -INFINITY};
   if (j < a.top) {
     x.id = a.ids[n * a.i_stride + j];
-    x.t = (float)((const TT *)a.teacher)[n * a.t_stride + j];
+    const int64_t at = n * a.t_stride + j;
+    x.t = a.t_type == BPE_F32    ? ((const float *)a.teacher)[at]
+          : a.t_type == BPE_BF16 ? (float)((const bf16_t *)a.teacher)[at]
+                                 : (float)((const f16_t *)a.teacher)[at];
   }
   return x;
 }
@@ -78,7 +82,7 @@ __device__ __forceinline__ Entry load_entry(const DistillArgs &a, int64_t n, int
 //   T^2 (sum e_j ((t_j - largest t) - (z_j - largest z)) / (T sum e_j) + log (sum z / sum t))
 // whose logarithm and sum are in 64 bits: it is the difference of values larger
 // than itself where the student is near the teacher.
-template <typename TS, typename TT, int NT>
+template <typename TS, int NT>
 __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   constexpr int E = 16 / sizeof(TS), U = 4, STEP = NT * E;
   constexpr int W = NT / 64;
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   const float k = kLog2e / a.temperature;
   uint32_t status = 0;
   auto valid = [&](const Entry &x) { return x.id >= 0 && x.id < V; };
-  const Entry first = load_entry<TT>(a, n, tid);
+  const Entry first = load_entry(a, n, tid);
   const float z_first = valid(first) ? (float)z[first.id] : 0.f;
   Soft x = kNothing;
   auto add = [&](const Vec<TS, E> &v) {
@@ -124,7 +128,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   }
   Soft t = kNothing;
   for (int j = tid; j < a.top; j += NT) {
-    const Entry y = j == tid ? first : load_entry<TT>(a, n, j);
+    const Entry y = j == tid ? first : load_entry(a, n, j);
     if (y.id < -1 || y.id >= V) status |= BPE_STATUS_BAD_ID;
     if (!valid(y)) continue;
     const float m = fmaxf(t.m, y.t);
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   const double by = 1.0 / (double)a.temperature;
   double sum = 0.0;
   for (int j = tid; j < a.top; j += NT) {
-    const Entry y = j == tid ? first : load_entry<TT>(a, n, j);
+    const Entry y = j == tid ? first : load_entry(a, n, j);
     if (!valid(y)) continue;
     const float zj = j == tid ? z_first : (float)z[y.id];
     const float e = power(y.t - t.m, k);
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
 // 28 for 16,000 rows of 876 with lists of 200).  4,096 rows of 128,256 bfloat16
 // logits, 2.1 GB, take 380 us, 5.5 TB/s, bound by memory; with the table as a word
 // per logit, 32 KB of LDS more, 418.
-template <typename TS, typename TT, typename TG, int NT, int S, bool STREAM>
+template <typename TS, typename TG, int NT, int S, bool STREAM>
 __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   constexpr int E = sizeof(TS) == 2 && sizeof(TG) == 2 ? 8 : 4;
   constexpr int U = 4;
@@ -211,7 +215,7 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   bool bad = false;
   // (the list is filled up to whole groups of 8 with entries that hold no token)
   for (int j = tid; j < top8; j += NT) {
-    const Entry y = load_entry<TT>(a, n, j);
+    const Entry y = load_entry(a, n, j);
     bad |= y.id < -1 || y.id >= a.vocab;
     ids[j] = y.id;
     parts[j] = y.id >= 0 ? power(y.t - tm, k) * by_ts : 0.f;
@@ -272,64 +276,51 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   }
 }
 
-template <typename TS, typename TT>
-hipError_t distill_launch(const DistillArgs &a, hipStream_t stream) {
+template <typename TS>
+hipError_t distill_as(const DistillArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)a.rows);
   if (a.vocab <= kDistillNarrow)
-    hipLaunchKernelGGL((k_distill<TS, TT, 64>), grid, dim3(64), 0, stream, a);
+    hipLaunchKernelGGL((k_distill<TS, 64>), grid, dim3(64), 0, stream, a);
   else
-    hipLaunchKernelGGL((k_distill<TS, TT, kDistillThreads>), grid, dim3(kDistillThreads), 0, stream, a);
+    hipLaunchKernelGGL((k_distill<TS, kDistillThreads>), grid, dim3(kDistillThreads), 0, stream, a);
   return hipGetLastError();
 }
 
-template <typename TS>
-hipError_t distill_as(const DistillArgs &a, int tt, hipStream_t stream) {
-  if (tt == BPE_F32) return distill_launch<TS, float>(a, stream);
-  if (tt == BPE_BF16) return distill_launch<TS, bf16_t>(a, stream);
-  return distill_launch<TS, f16_t>(a, stream);
-}
-
-template <typename TS, typename TT, typename TG, int NT, int S>
+template <typename TS, typename TG, int NT, int S>
 hipError_t grad_slabs(const DistillArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.vocab + S - 1) / S * a.rows));
   const size_t lds = (a.top + 7) / 8 * 8 * 3 * sizeof(int32_t);
   const bool big = a.rows * a.vocab * (int64_t)sizeof(TG) >= kStreamBytes;
   if (big)
-    hipLaunchKernelGGL((k_distill_grad<TS, TT, TG, NT, S, true>), grid, dim3(NT), lds, stream, a);
+    hipLaunchKernelGGL((k_distill_grad<TS, TG, NT, S, true>), grid, dim3(NT), lds, stream, a);
   else
-    hipLaunchKernelGGL((k_distill_grad<TS, TT, TG, NT, S, false>), grid, dim3(NT), lds, stream, a);
+    hipLaunchKernelGGL((k_distill_grad<TS, TG, NT, S, false>), grid, dim3(NT), lds, stream, a);
   return hipGetLastError();
 }
-template <typename TS, typename TT, typename TG>
+template <typename TS, typename TG>
 hipError_t grad_launch(const DistillArgs &a, hipStream_t stream) {
-  return a.vocab <= kDistillNarrow ? grad_slabs<TS, TT, TG, 64, kDistillNarrow>(a, stream)
-                                   : grad_slabs<TS, TT, TG, kDistillThreads, kDistillSlab>(a, stream);
-}
-template <typename TS, typename TT>
-hipError_t grad_from(const DistillArgs &a, int gt, hipStream_t stream) {
-  if (gt == BPE_F32) return grad_launch<TS, TT, float>(a, stream);
-  if (gt == BPE_BF16) return grad_launch<TS, TT, bf16_t>(a, stream);
-  return grad_launch<TS, TT, f16_t>(a, stream);
+  return a.vocab <= kDistillNarrow ? grad_slabs<TS, TG, 64, kDistillNarrow>(a, stream)
+                                   : grad_slabs<TS, TG, kDistillThreads, kDistillSlab>(a, stream);
 }
 template <typename TS>
-hipError_t grad_as(const DistillArgs &a, int tt, int gt, hipStream_t stream) {
-  if (tt == BPE_F32) return grad_from<TS, float>(a, gt, stream);
-  if (tt == BPE_BF16) return grad_from<TS, bf16_t>(a, gt, stream);
-  return grad_from<TS, f16_t>(a, gt, stream);
+hipError_t grad_as(const DistillArgs &a, int gt, hipStream_t stream) {
+  if (gt == BPE_F32) return grad_launch<TS, float>(a, stream);
+  if (gt == BPE_BF16) return grad_launch<TS, bf16_t>(a, stream);
+  return grad_launch<TS, f16_t>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_distill(const DistillArgs &a, int st, int tt, hipStream_t stream) {
-  if (st == BPE_F32) return distill_as<float>(a, tt, stream);
-  if (st == BPE_BF16) return distill_as<bf16_t>(a, tt, stream);
-  return distill_as<f16_t>(a, tt, stream);
+hipError_t launch_distill(const DistillArgs &a, int st, hipStream_t stream) {
+  if (st == BPE_F32) return distill_as<float>(a, stream);
+  if (st == BPE_BF16) return distill_as<bf16_t>(a, stream);
+  return distill_as<f16_t>(a, stream);
 }
 
-hipError_t launch_distill_grad(const DistillArgs &a, int st, int tt, int gt, hipStream_t stream) {
-  if (st == BPE_F32) return grad_as<float>(a, tt, gt, stream);
-  if (st == BPE_BF16) return grad_as<bf16_t>(a, tt, gt, stream);
-  return grad_as<f16_t>(a, tt, gt, stream);
+hipError_t launch_distill_grad(const DistillArgs &a, int st, int gt, hipStream_t stream) {
+  if (st == BPE_F32) return grad_as<float>(a, gt, stream);
+  if (st == BPE_BF16) return grad_as<bf16_t>(a, gt, stream);
+  return grad_as<f16_t>(a, gt, stream);
 }
 
 }  // namespace bpe

@@ -263,7 +263,7 @@ struct DistillArgs {
   int64_t rows, vocab, s_stride, t_stride;
   const int32_t *ids;
   int64_t i_stride;
-  int32_t top;
+  int32_t top, t_type;
   float temperature;
   float *losses, *stats;       // the loss's
   const float *in_stats, *dloss;  // the gradient's
@@ -273,7 +273,7 @@ struct DistillArgs {
 };
 
 bool distill_grad_fits(int64_t n_rows, int64_t vocab);
-hipError_t launch_distill(const DistillArgs &a, int st, int tt, hipStream_t stream);
-hipError_t launch_distill_grad(const DistillArgs &a, int st, int tt, int gt, hipStream_t stream);
+hipError_t launch_distill(const DistillArgs &a, int st, hipStream_t stream);
+hipError_t launch_distill_grad(const DistillArgs &a, int st, int gt, hipStream_t stream);
 
 }  // namespace bpe

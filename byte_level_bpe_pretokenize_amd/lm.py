@@ -790,5 +790,6 @@ def distillation(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor
                  temperature: float = 1.0, *, status: torch.Tensor | None = None) -> torch.Tensor:
     """``distill``'s losses with ``distill_grad`` as their gradient for autograd, on
     the current stream.  The teacher gets no gradient."""
-    _no_gradient("distillation's teacher", "call it ", (teacher,))
+    if teacher.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError("distillation gives no gradient to the teacher, which requires one: detach it")
     return _Distillation.apply(student, ids, teacher, temperature, status)
