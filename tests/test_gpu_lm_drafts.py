@@ -114,6 +114,15 @@ def test_samples_outside():
     assert got.tolist() == [1, 1, 4, 4, 4, 1]
 
 
+def test_accepts_outside():
+    p, q, ids, off, accept, sample = batch([6] * 8, 300, F32, 4)
+    for x, n in ((-1.0, 7), (float("nan"), 1), (float("inf"), 1), (-float("inf"), 7)):
+        accept[:] = x
+        q[:, 5] += 1e-6  # (no draft's probability is 0)
+        _, counts = check(p, q, ids, off, accept, sample)
+        assert counts.tolist() == [n] * 8
+
+
 @pytest.mark.parametrize("V", [4000, 70000])
 def test_what_is_no_probability(V):
     """Negative entries, infinities and NaN count as 0; nothing left of the difference
@@ -275,6 +284,23 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         want, n = ref.verify(f64(p), ids.cpu().numpy(), off, accept.cpu().numpy(), sample.cpu().numpy(), f64(q))
         assert np.array_equal(tokens.cpu().numpy(), want) and np.array_equal(counts.cpu().numpy(), n)
+    assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("V", [9000, 70000])
+def test_two_streams_at_once(V):
+    args = [batch([4, 1, 0, 7], V, F32, k) for k in range(2)]
+    offs = [dev(a[3]) for a in args]
+    want = [lm.verify_drafts(a[0], a[2], o, a[4], a[5], draft=a[1]) for a, o in zip(args, offs)]
+    streams, st = [torch.cuda.Stream() for _ in range(2)], status()
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for k, (a, o, s) in enumerate(zip(args, offs, streams)):
+            got[k].append(lm.verify_drafts(a[0], a[2], o, a[4], a[5], draft=a[1], status=st, stream=s))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(x, want[k][0]) and torch.equal(n, want[k][1]) for x, n in got[k])
     assert int(st.item()) == 0
 
 
