@@ -243,7 +243,7 @@ int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t
   a.status = d_status;
   a.x = d_x;
   a.slots = d_slots;
-  cache_shape(&a, true);
+  cache_shape(&a, true, x_type);
   if (!cache_fits(a)) return BPE_EINVAL;
   return launch_cache_write(a, x_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }
@@ -274,7 +274,7 @@ int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_req
   a.width = table_width;
   a.stride = table_stride;
   a.bs = divisor(block_size);
-  cache_shape(&a, false);
+  cache_shape(&a, false, out_type);
   if (!cache_fits(a)) return BPE_EINVAL;
   return launch_cache_read(a, out_type, (hipStream_t)hip_stream) == hipSuccess ? BPE_OK : BPE_EHIP;
 }

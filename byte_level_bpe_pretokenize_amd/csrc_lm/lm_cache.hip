@@ -23,20 +23,11 @@ __device__ __forceinline__ Vec<T, E> load_some(const T *p, int m) {
   for (int e = 0; e < E; ++e) r.v[e] = e < m ? p[e] : (T)0.f;
   return r;
 }
-template <typename T>
-__device__ __forceinline__ void store_some(T *p, const Vec<T, E> &x, int m) {
-  if (m >= E) {
-    store_vec<T, E>(p, x);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (e < m) p[e] = x.v[e];
-}
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 // Bytes in device memory, at any address.
+typedef uint16_t b2 __attribute__((aligned(1)));
 typedef uint32_t b4 __attribute__((aligned(1)));
 typedef uint32_t b8 __attribute__((ext_vector_type(2), aligned(1)));
 
@@ -226,21 +217,24 @@ __global__ void __launch_bounds__(CT) k_cache_write(CacheArgs a) {
   if (status) atomicOr(a.status, (int32_t)status);
 }
 
-// The values of E codes (of E / 2 bytes for BPE_UINT4: the lower and the upper
-// halves apart, since a byte to a float is one instruction).
+// ---- reading: N elements a lane (cache_read_vec) ----
+
 struct Step {
   float scale, low;
 };
-template <int F, typename T, typename S>
-__device__ __forceinline__ Vec<T, E> decode(const uint32_t *w, S step) {
-  Vec<T, E> r;
+
+// The values of N codes (of N / 2 bytes for BPE_UINT4: the lower and the upper
+// halves apart, since a byte to a float is one instruction).
+template <int F, typename T, int N, typename S>
+__device__ __forceinline__ Vec<T, N> decode(const uint32_t *w, S step) {
+  Vec<T, N> r;
   uint32_t b[2];
   if (F == BPE_UINT4) {
     b[0] = w[0] & 0x0f0f0f0fu;
     b[1] = w[0] >> 4 & 0x0f0f0f0fu;
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
+  for (int e = 0; e < N; ++e) {
     float y;
     const Step x = step(e);
     if (F == BPE_E4M3) {
@@ -260,28 +254,31 @@ __device__ __forceinline__ Vec<T, E> decode(const uint32_t *w, S step) {
   return r;
 }
 
-// The codes of the E elements from c on of a head's row q; of BPE_UINT4 c may be odd
+// The codes of the N elements from c on of a head's row q; of BPE_UINT4 c may be odd
 // where they are the head's last.
-template <int F, bool WHOLE>
+template <int F, int N, bool WHOLE>
 __device__ __forceinline__ void load_codes(const uint8_t *q, int c, uint32_t *w) {
   if (F == BPE_UINT4) {
-    w[0] = *(const b4 *)(q + (c >> 1));
+    const uint8_t *at = q + (c >> 1);
+    w[0] = N == 8 ? *(const b4 *)at : (uint32_t)*(const b2 *)at;
     if (!WHOLE) {
-      const uint32_t after = q[(c + E - 1) >> 1];
-      if (c & 1) w[0] = w[0] >> 4 | after << 28;
+      const uint32_t after = q[(c + N - 1) >> 1];
+      if (c & 1) w[0] = w[0] >> 4 | after << (4 * N - 4);
     }
-  } else {
+  } else if (N == 8) {
     const b8 x = *(const b8 *)(q + c);
     w[0] = x.x;
     w[1] = x.y;
+  } else {
+    w[0] = *(const b4 *)(q + c);
   }
 }
-// Those of a head of dim < E elements.
-template <int F>
+// Those of a head of dim < N elements.
+template <int F, int N>
 __device__ __forceinline__ void load_few(const uint8_t *q, int dim, uint32_t *w) {
   w[0] = w[1] = 0;
 #pragma unroll
-  for (int e = 0; e < (F == BPE_UINT4 ? E / 2 : E); ++e)
+  for (int e = 0; e < (F == BPE_UINT4 ? N / 2 : N); ++e)
     if ((F == BPE_UINT4 ? 2 * e : e) < dim) w[e >> 2] |= (uint32_t)q[e] << 8 * (e & 3);
 }
 
@@ -292,7 +289,7 @@ __device__ __forceinline__ void load_few(const uint8_t *q, int dim, uint32_t *w)
 // 5.1 TB/s, bound by memory (760 with one vector at a time, loaded by bytes).  1,800
 // tokens of 16 heads of 64: 4.4 us, a chain of five dependent accesses.  Heads of no
 // whole vectors: 60,000 tokens of 64 heads of 77 in e4m3 3.5 TB/s, and of 80 4.8.
-template <typename T, int F, bool WHOLE, bool STREAM>
+template <typename T, int F, int N, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
   constexpr int64_t kNot = INT64_MIN;  // no request's
   __shared__ int64_t slots[kCacheTokens];
@@ -331,7 +328,7 @@ __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
   constexpr int U = 4;
   for (int base = 0; base < count; base += CT * U) {
     // All loads first, unconditional ones, so that they are in flight together.
-    // Heads of no whole vectors: the last vector is the head's last E elements, some
+    // Heads of no whole vectors: the last vector is the head's last N elements, some
     // of which the one before it has too (both store the same); it may have two
     // groups' elements.
     int64_t at[U], slot[U];
@@ -344,8 +341,8 @@ __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
       const int token = divide(a.per_token, i);
       const int k = i - token * a.per_token.d;
       const int head = divide(a.per_head, k);
-      int c = (k - head * a.per_head.d) * E;
-      if (!WHOLE) c = max(min(c, a.c.dim - E), 0);
+      int c = (k - head * a.per_head.d) * N;
+      if (!WHOLE) c = max(min(c, a.c.dim - N), 0);
       slot[u] = slots[token];
       at[u] = (t0 + token) * a.t_stride + head * a.h_stride + c;
       const uint8_t *q = (const uint8_t *)a.c.codes + slot[u] * a.c.codes_stride + head * a.row_bytes;
@@ -354,9 +351,9 @@ __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
         q = (const uint8_t *)a.off - (F == BPE_UINT4 ? c >> 1 : c);
         s = (const float *)a.off - (c >> a.group_log2) * (F == BPE_UINT4 ? 2 : 1);
       }
-      if (WHOLE || a.c.dim >= E) load_codes<F, WHOLE>(q, c, w[u]);
-      else load_few<F>(q, a.c.dim, w[u]);
-      const int g = c >> a.group_log2, h = WHOLE ? g : min(c + E - 1, a.c.dim - 1) >> a.group_log2;
+      if (WHOLE || a.c.dim >= N) load_codes<F, N, WHOLE>(q, c, w[u]);
+      else load_few<F, N>(q, a.c.dim, w[u]);
+      const int g = c >> a.group_log2, h = WHOLE ? g : min(c + N - 1, a.c.dim - 1) >> a.group_log2;
       auto load_step = [&](int g) {
         return F == BPE_UINT4 ? Step{s[2 * g], s[2 * g + 1]} : Step{s[g], 0.f};
       };
@@ -366,12 +363,17 @@ __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      Vec<T, E> y = decode<F, T>(w[u], [&](int e) { return WHOLE || e < edge[u] ? first[u] : second[u]; });
-      if (slot[u] < 0) y = Vec<T, E>{};
+      Vec<T, N> y = decode<F, T, N>(w[u], [&](int e) { return WHOLE || e < edge[u] ? first[u] : second[u]; });
+      if (slot[u] < 0) y = Vec<T, N>{};
       if (base + u * CT + tid >= count || slot[u] == kNot) continue;
       T *out = (T *)a.out + at[u];
-      if (WHOLE || a.c.dim >= E) store_vec<T, E, STREAM>(out, y);
-      else store_some(out, y, a.c.dim);
+      if (WHOLE || a.c.dim >= N) {
+        store_vec<T, N, STREAM>(out, y);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (e < a.c.dim) out[e] = y.v[e];
+      }
     }
   }
   if (status) atomicOr(a.status, (int32_t)status);
@@ -387,13 +389,14 @@ hipError_t write_launch(const CacheArgs &a, hipStream_t stream) {
 template <typename T, int F>
 hipError_t read_launch(const CacheArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)cache_workgroups(a)), wg(CT);
+  constexpr int N = 16 / sizeof(T);
   const bool big = a.n * a.c.heads * a.c.dim * (int64_t)sizeof(T) >= kStreamBytes;
-  if (a.c.dim % E != 0)
-    hipLaunchKernelGGL((k_cache_read<T, F, false, false>), grid, wg, 0, stream, a);
+  if (a.c.dim % N != 0)
+    hipLaunchKernelGGL((k_cache_read<T, F, 8, false, false>), grid, wg, 0, stream, a);
   else if (big)
-    hipLaunchKernelGGL((k_cache_read<T, F, true, true>), grid, wg, 0, stream, a);
+    hipLaunchKernelGGL((k_cache_read<T, F, N, true, true>), grid, wg, 0, stream, a);
   else
-    hipLaunchKernelGGL((k_cache_read<T, F, true, false>), grid, wg, 0, stream, a);
+    hipLaunchKernelGGL((k_cache_read<T, F, N, true, false>), grid, wg, 0, stream, a);
   return hipGetLastError();
 }
 

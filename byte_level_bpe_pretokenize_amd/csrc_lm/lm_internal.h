@@ -145,7 +145,7 @@ hipError_t launch_blocks(const BlockArgs &a, hipStream_t stream);
 
 // ---- a cache of few bits -----------------------------------------------------------
 constexpr int kCacheThreads = 256;
-constexpr int kCacheVec = 8;       // elements per lane
+constexpr int kCacheVec = 8;       // elements per lane of a write
 constexpr int kCacheTokens = 64;   // tokens per workgroup, at most
 constexpr int kCacheMinGroup = 16, kCacheMaxGroup = 64 * kCacheVec;  // a wave's lanes at most
 
@@ -164,8 +164,8 @@ struct CacheArgs {
   int64_t n;              // tokens
   int64_t t_stride, h_stride;
   int32_t *status;
-  // a token's lanes, kCacheVec elements each: lanes per head and per token (a
-  // write has whole groups of lanes per group of elements)
+  // a token's lanes: per head and per token (kCacheVec elements each and whole groups
+  // of lanes per group of elements in a write, cache_read_vec elements in a read)
   Divisor per_head, per_token;
   int32_t tokens;         // per workgroup
   // write
@@ -183,7 +183,8 @@ int32_t cache_groups(const bpe_cache &c);
 int32_t cache_row_bytes(const bpe_cache &c);
 bool cache_ok(const bpe_cache &c);
 bool cache_tokens_ok(const bpe_cache &c, int64_t n, int64_t token_stride, int64_t head_stride);
-void cache_shape(CacheArgs *a, bool write);
+int32_t cache_read_vec(int32_t dim, int out_type);
+void cache_shape(CacheArgs *a, bool write, int out_type);
 bool cache_fits(const CacheArgs &a);  // (shaped)
 inline int64_t cache_workgroups(const CacheArgs &a) { return (a.n + a.tokens - 1) / a.tokens; }
 

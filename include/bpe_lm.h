@@ -285,7 +285,8 @@ int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t
  *           (BPE_STATUS_TABLE_FULL), past slot n_slots (BPE_STATUS_BAD_SLOT) and
  *           past position INT32_MAX (BPE_STATUS_BAD_LENGTH).
  *  d_out    [n][heads][dim] of out_type, strides as those of d_x.
- * n <= 2^30 - 64, n * heads * ceil(dim / 8) < 2^33, n_requests <= 2^30.
+ * n <= 2^30 - 64, n * heads * ceil(dim / 8) < 2^33 (float32 of dim a multiple of
+ * 4: dim / 4), n_requests <= 2^30.
  * Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */
 int bpe_cache_read(const bpe_cache *cache, const int32_t *d_table, int64_t n_requests,

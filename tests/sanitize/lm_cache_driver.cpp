@@ -40,11 +40,12 @@ static void shape() {
     a.c.group = kCacheMinGroup << below(6);
     a.c.format = (int)below(3);
     for (bool write : {true, false}) {
-      cache_shape(&a, write);
+      const int ot = (int)below(3), vec = write ? kCacheVec : cache_read_vec(a.c.dim, ot);
+      cache_shape(&a, write, ot);
       CHECK(1 << a.group_log2 == a.c.group);
       CHECK(a.groups * a.c.group >= a.c.dim && (a.groups - 1) * a.c.group < a.c.dim);
-      CHECK(a.per_head.d * kCacheVec >= a.c.dim);
-      CHECK(a.per_token.d == a.per_head.d * a.c.heads && a.per_token.d <= 1 << 17);
+      CHECK(a.per_head.d * vec >= a.c.dim);
+      CHECK(a.per_token.d == a.per_head.d * a.c.heads && a.per_token.d <= 1 << 18);
       CHECK(a.tokens >= 1 && a.tokens <= kCacheTokens);
       if (write) {
         const int lanes = a.c.group / kCacheVec;
@@ -115,10 +116,11 @@ static void limit() {
     a.c.dim = i % 5 ? 1 + (int)below(BPE_MAX_DIM) : 1 + (int)below(40);
     a.c.group = kCacheMinGroup << below(6);
     const bool write = i % 2;
-    cache_shape(&a, write);
+    const int ot = (int)below(3), vec = ot == BPE_F32 && a.c.dim % 4 == 0 ? 4 : 8;
+    cache_shape(&a, write, ot);
     const int64_t most = BPE_MAX_IDS - kCacheTokens;
     a.n = i % 7 ? std::min(most, ((int64_t)1 << 33) / a.per_token.d + below(5) - 2) : 1 + below(most);
-    const int64_t per = write ? (int64_t)a.groups * a.c.group / 8 : (a.c.dim + 7) / 8;
+    const int64_t per = write ? (int64_t)a.groups * a.c.group / 8 : (a.c.dim + vec - 1) / vec;
     CHECK(cache_fits(a) == (a.n * a.c.heads * per < (int64_t)1 << 33));
     if (!cache_fits(a)) {
       ++not_;
