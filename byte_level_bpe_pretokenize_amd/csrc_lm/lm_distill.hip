@@ -52,6 +52,14 @@ __device__ __forceinline__ Soft wave_soft(Soft x, float k) {
   return Soft{m, wave_total(x.s * power(x.m - m, k))};
 }
 
+// Elements of p[0 .. n) before its first 16-byte boundary.  Rows of odd width start
+// anywhere: 4,096 rows of 50,257 bfloat16 logits take 75 us with vectors from the
+// boundary on, 92 from the row's start (float32: no difference; short rows: slower).
+template <typename T>
+__device__ __forceinline__ int before_16(const T *p, int n) {
+  return min(n, (int)((0 - (uintptr_t)p) & 15) / (int)sizeof(T));
+}
+
 // An entry of a teacher's row: its token's place, or -1.
 struct Entry {
   int32_t id;
@@ -108,7 +116,15 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     x.s = x.s * power(x.m - m, k) + s;
     x.m = m;
   };
-  int v = 0;
+  // whole lines: what comes before the row's first 16-byte boundary is added alone
+  const int head = sizeof(TS) == 2 && NT > 64 ? before_16(z, V) : 0;
+  if (tid < head) {
+    Vec<TS, E> y;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y.v[e] = e == 0 ? z[tid] : (TS)-INFINITY;
+    add(y);
+  }
+  int v = head;
   for (; v + STEP * U <= V; v += STEP * U) {
     Vec<TS, E> y[U];
 #pragma unroll
