@@ -500,8 +500,11 @@ def _cache(codes: torch.Tensor, scales: torch.Tensor, group: int, heads: int, di
         raise TypeError(f"codes: float8_e4m3fn, int8 or uint8 expected, got {codes.dtype}")
     if scales.dtype is not torch.float32:
         raise TypeError(f"scales: torch.float32 expected, got {scales.dtype}")
-    if group < 1:
-        raise ValueError(f"group: {group} is out of range")
+    # (32 bits each in bpe_cache, which ctypes would fill with what is left of more)
+    if not (1 <= group < 1 << 31 and heads < 1 << 31 and dim < 1 << 31):
+        _int32(group, 1, "group")
+        _int32(heads, 0, "heads")
+        _int32(dim, 0, "dim")
     shape, n = scales.shape, codes.shape[0]
     G = (dim + group - 1) // group
     if form == _lib.UINT4:
