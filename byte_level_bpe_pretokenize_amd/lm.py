@@ -547,7 +547,7 @@ def cache_write(x: torch.Tensor, slots: torch.Tensor, codes: torch.Tensor, scale
     if stream is not None:
         return _on(stream, cache_write, (x, slots, codes, scales, status), x, slots, codes, scales,
                    group, status=status)
-    _no_gradient("cache_write", "call it ", (x, scales))
+    _no_gradient("cache_write", "call it ", (x, codes, scales))
     xt = _type(x.dtype, "x")
     if x.dim() != 3:
         raise ValueError(f"x: (n, heads, dim) expected, got {x.dim()} dimensions")
@@ -579,7 +579,7 @@ def cache_read(codes: torch.Tensor, scales: torch.Tensor, group: int, table: tor
         kw = dict(start=start, out=out, status=status)
         return _on(stream, cache_read, (codes, scales, table, off, *kw.values()), codes, scales, group,
                    table, block_size, off, n, dim=dim, out_dtype=out_dtype, **kw)
-    _no_gradient("cache_read", "call it ", (scales, out))
+    _no_gradient("cache_read", "call it ", (codes, scales, out))
     if codes.dim() != 3:
         raise ValueError(f"codes: 3 dimensions expected, got {codes.dim()}")
     H = codes.shape[1]
@@ -713,7 +713,7 @@ def distill(student: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, tem
         kw = dict(losses=losses, stats=stats, status=status)
         return _on(stream, distill, (student, ids, teacher, *kw.values()), student, ids, teacher,
                    temperature, **kw)
-    _no_gradient("distill", "call distillation instead, or distill ", (student, teacher))
+    _no_gradient("distill", "call distillation instead, or distill ", (student, teacher, losses, stats))
     a = _teacher(student, ids, teacher)
     N = a[2]
     if losses is not None:
