@@ -207,7 +207,8 @@ def serve_drafts(model, special, weight, drafter, texts, steps: int = 6, k: int 
         tokens, counts = lm.verify_drafts(torch.softmax(logits, 1), drafted.reshape(-1), rows_off, accept.view(-1),
                                           sample, draft=q.view(-1, V), status=status)
         tokens = tokens.view(R, k + 1)
-        last = tokens.gather(1, counts.long()[:, None] - 1)[:, 0]
+        # (a request without a token, which the status tells of, goes on from the -1 it got)
+        last = tokens.gather(1, (counts.long()[:, None] - 1).clamp(min=0))[:, 0]
         # what does not stand leaves the cache: its blocks are free again
         want, lengths = (lengths + BLOCK - 1) // BLOCK, before + counts
         back = (at >= ((lengths + BLOCK - 1) // BLOCK)[:, None]) & (at < want[:, None])
