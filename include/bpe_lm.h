@@ -321,8 +321,10 @@ size_t bpe_verify_drafts_workspace_bytes(int64_t n_requests, int64_t vocab);
  *           request's last row of d_draft is never read.  d_draft NULL: the
  *           drafts were certain (q is 1 at x_i and 0 elsewhere).
  *  accept, sample      float [n_rows], [n_requests], uniform in [0, 1).  An accept
- *           outside is compared as it is (below 0 every token stands, NaN none);
- *           a sample outside takes the nearer end (NaN the upper).
+ *           outside is compared as it is.  Below 0: a token with q > 0 stands
+ *           whatever p is, one with q = 0 (what counts as 0 included) if p > 0, or
+ *           not at all for -infinity, whose product with 0 is NaN.  NaN: none
+ *           stands.  A sample outside takes the nearer end (NaN the upper).
  * A drafted token outside [0, vocab) that comes to be looked at sets
  * BPE_STATUS_BAD_ID and does not stand.  Offsets that decrease or leave
  * [0, n_rows] set BPE_STATUS_BAD_ID_OFFSETS, and their request counts as one
