@@ -3,8 +3,13 @@ import numpy as np
 import pytest
 import torch
 
+import lm_draft_reference as ref
+from lm_reference import f64
+from byte_level_bpe_pretokenize_amd import _lib, lm
+
 from gpu_util import device
-from test_gpu_lm_drafts import check
+from test_gpu_lm import F32, dev, status
+from test_gpu_lm_drafts import batch, check
 from test_gpu_lm_example import example
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +47,32 @@ def test_accepts_outside_against_drafts_without_probability(accept, V):
     else:
         want = [1] * 10
     assert counts.tolist() == want
+
+
+@pytest.mark.parametrize("V", [100, 70000])
+def test_requests_beside_bad_offsets_keep_their_tokens(V):
+    """Requests whose offsets are valid and that share no row with another one get
+    what they get alone; rows that are no request's are left as they were."""
+    p, q, ids, _, accept, sample = batch([4, 4, 4], V, F32, 1)
+    for off, fine in (([0, 5, 3, 15], (0,)), ([0, 5, 10, 16], (0, 1)), ([-1, 5, 10, 15], (1, 2)),
+                      ([2 ** 62, -2 ** 62, 10, 15], (2,)), ([7, 6, 5, 15], (2,))):
+        tokens, st = torch.full((15,), -9, dtype=torch.int32, device=device()), status()
+        _, counts = lm.verify_drafts(p, ids, dev(np.array(off, np.int64)), accept, sample, draft=q, tokens=tokens,
+                                     status=st)
+        assert int(st.item()) == _lib.STATUS_BAD_ID_OFFSETS
+        left = np.ones(15, bool)
+        for r in range(3):
+            lo, hi = off[r], off[r + 1]
+            if r not in fine:
+                # (3 to 15 is a request by itself, though it has rows of the first one)
+                if not 0 <= lo <= hi <= 15:
+                    assert int(counts[r]) == 0
+                else:
+                    left[lo:hi] = False
+                continue
+            want, n = ref.verify(f64(p), ids.cpu().numpy(), [lo, hi], accept.cpu().numpy(),
+                                 sample[r:r + 1].cpu().numpy(), f64(q))
+            rows = slice(lo, 3 if off[2] == 3 else hi)  # (the rows that no other request has)
+            assert int(counts[r]) == n[0] and np.array_equal(tokens.cpu().numpy()[rows], want[rows])
+            left[lo:hi] = False
+        assert bool((tokens.cpu()[torch.from_numpy(left)] == -9).all())
