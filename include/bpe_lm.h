@@ -285,6 +285,8 @@ int bpe_cache_write(const bpe_cache *cache, const void *d_x, int x_type, int64_t
  *           (BPE_STATUS_TABLE_FULL), past slot n_slots (BPE_STATUS_BAD_SLOT) and
  *           past position INT32_MAX (BPE_STATUS_BAD_LENGTH).
  *  d_out    [n][heads][dim] of out_type, strides as those of d_x.
+ * Without tokens or requests (n or n_requests 0) nothing is launched, and what is
+ * wrong with the offsets or starts then is not looked for.
  * n <= 2^30 - 64, n * heads * ceil(dim / 8) < 2^33 (float32 of dim a multiple of
  * 4: dim / 4), n_requests <= 2^30.
  * Returns BPE_OK, BPE_EINVAL or BPE_EHIP.

@@ -76,3 +76,15 @@ def test_requests_beside_bad_offsets_keep_their_tokens(V):
             assert int(counts[r]) == n[0] and np.array_equal(tokens.cpu().numpy()[rows], want[rows])
             left[lo:hi] = False
         assert bool((tokens.cpu()[torch.from_numpy(left)] == -9).all())
+
+
+def test_a_read_of_no_tokens_looks_at_nothing():
+    """No launch, so no status: offsets past the tokens and a negative start."""
+    c, s, group = lm.empty_cache(8, 2, 16, torch.int8, device=device())
+    table, st = torch.zeros((2, 1), dtype=torch.int32, device=device()), status()
+    for off in ([0, 5, 9], [3, 2, 1], [-1, 0, 0]):
+        got = lm.cache_read(c, s, group, table, 4, dev(np.array(off, np.int64)), 0,
+                            start=dev(np.array([-1, -1], np.int32)), status=st)
+        assert got.shape == (0, 2, 16)
+    none = lm.cache_read(c, s, group, table[:0], 4, dev(np.array([7], np.int64)), 3, status=st)
+    assert none.shape == (3, 2, 16) and int(st.item()) == 0
