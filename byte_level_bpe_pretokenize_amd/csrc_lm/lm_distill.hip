@@ -79,6 +79,77 @@ __device__ __forceinline__ Entry load_entry(const DistillArgs &a, int64_t n, int
   return x;
 }
 
+// The sum over a workgroup's threads, in each of them.
+template <int NT>
+__device__ __forceinline__ double group_sum(double x, double *lds) {
+  x = wave_sum(x);
+  if (NT == 64) return x;
+  __syncthreads();
+  if (lane_id() == 0) lds[wave_id()] = x;
+  __syncthreads();
+  x = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) x += lds[w];
+  return x;
+}
+
+// ---- warm rows ------------------------------------------------------------------
+// A loss is T^2 times a divergence that falls with T^2 where the listed tokens are
+// (nearly) all that the student gives anything to, and a gradient T times a difference
+// that falls with T.  From sums in 32 bits, which are off by some 2^-23, a loss of
+// 0.005 over 1,000 of 1,000 tokens came out off by 0.5% at T = 32, by its double at
+// 256, and negative at 4,096.  So above kDistillWarm, where the listed tokens hold
+// more than 3 / 4 of the student's sum, both come from the tokens' differences, each
+// of which is exact in 64 bits: with e_j = exp((t_j - largest t) / T), f_j the same of
+// the student's listed z_j, d_j = ((t_j - largest t) - (z_j - largest z)) / T, mean
+// and sums over the list weighted by e,
+//   loss / T^2 = log(1 + sum e_j (exp(x_j) - 1 - x_j) / sum e_j) + log(1 + rest / sum f_j)
+//   x_j = mean d - d_j,   log(q_j / P_j) = x_j - loss / T^2
+// with rest the student's sum less sum f_j.  No term of the first logarithm is negative,
+// so e's roundings (32 bits) are relative to it.  The rest is the sum over all logits,
+// read again now that the largest is known, less that over the listed ones: of the
+// same 32-bit values, added in 64 bits, so that what is listed leaves nothing.  (With
+// more rest the loss is T^2 / 4 at least, and sums in 32 bits are near enough.)
+struct Near {
+  double mean, loss;  // (loss: infinite or NaN where a listed logit is; of the row / T^2)
+};
+// get(j, &e, &f, &d): entry j's, and whether it holds a token with e > 0.  held: sum f.
+template <typename TS, int NT, typename F>
+__device__ __forceinline__ Near near_teacher(F get, int top, const TS *z, int V, float zm, float k, double held,
+                                             double *lds) {
+  constexpr int E = 16 / sizeof(TS);
+  const int tid = threadIdx.x;
+  float e, f;
+  double d, weight = 0.0, sum = 0.0, all = 0.0;
+  for (int j = tid; j < top; j += NT) {
+    if (!get(j, &e, &f, &d)) continue;
+    weight += (double)e;
+    sum += (double)e * d;
+  }
+  weight = group_sum<NT>(weight, lds);
+  Near r;
+  r.mean = group_sum<NT>(sum, lds) / weight;
+  sum = 0.0;
+  for (int j = tid; j < top; j += NT) {
+    if (!get(j, &e, &f, &d)) continue;
+    const double x = r.mean - d;
+    sum += (double)e * (expm1(x) - x);
+  }
+  sum = group_sum<NT>(sum, lds) / weight;
+  for (int v = tid * E; v < V; v += NT * E) {
+    if (v + E <= V) {
+      const Vec<TS, E> y = load_vec<TS, E>(z + v);
+#pragma unroll
+      for (int i = 0; i < E; ++i) all += (double)power((float)y.v[i] - zm, k);
+    } else {
+      for (int i = v; i < V; ++i) all += (double)power((float)z[i] - zm, k);
+    }
+  }
+  all = group_sum<NT>(all, lds);
+  r.loss = log1p(sum) + log1p((all - held) / held);
+  return r;
+}
+
 // A workgroup per row: one pass over the logits with a running maximum and sum
 // per thread, joined over the workgroup; the listed logits are gathered before.
 // 4,096 rows of 128,256 bfloat16 logits, 1.05 GB, take 182 us, 5.8 TB/s, bound by
@@ -89,8 +160,8 @@ __device__ __forceinline__ Entry load_entry(const DistillArgs &a, int64_t n, int
 // With e_j = exp((t_j - largest t) / T), the loss is
 //   T^2 (sum e_j ((t_j - largest t) - (z_j - largest z)) / (T sum e_j) + log (sum z / sum t))
 // whose logarithm and sum are in 64 bits: it is the difference of values larger
-// than itself where the student is near the teacher.
-template <typename TS, int NT>
+// than itself where the student is near the teacher.  WARM: see above.
+template <typename TS, int NT, bool WARM>
 __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
   constexpr int E = 16 / sizeof(TS), U = 4, STEP = NT * E;
   constexpr int W = NT / 64;
@@ -163,13 +234,31 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     t = wave_soft(lane < W ? soft_t[lane] : kNothing, k);
   }
   const double by = 1.0 / (double)a.temperature;
-  double sum = 0.0;
+  double sum = 0.0, held = 0.0;
   for (int j = tid; j < a.top; j += NT) {
     const Entry y = j == tid ? first : load_entry(a, n, j);
     if (!valid(y)) continue;
     const float zj = j == tid ? z_first : (float)z[y.id];
     const float e = power(y.t - t.m, k);
     if (e != 0.f) sum += (double)e * (((double)y.t - t.m) - ((double)zj - x.m));
+    if (WARM && e != 0.f) held += (double)power(zj - x.m, k);
+  }
+  double warm = INFINITY;
+  if (WARM) {
+    held = group_sum<NT>(held, terms);
+    if (held > 0.75 * (double)x.s) {  // (the same in every thread)
+      auto get = [&](int j, float *e, float *f, double *d) {
+        const Entry y = load_entry(a, n, j);
+        if (!valid(y)) return false;
+        const float zj = (float)z[y.id];
+        *e = power(y.t - t.m, k);
+        *f = power(zj - x.m, k);
+        *d = (((double)y.t - t.m) - ((double)zj - x.m)) * by;
+        return *e != 0.f;
+      };
+      warm = near_teacher<TS, NT>(get, a.top, z, V, x.m, k, held, terms).loss;
+    }
+    if (W > 1) __syncthreads();  // (terms)
   }
   sum = wave_sum(sum);
   if (W > 1) {
@@ -183,7 +272,8 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
     }
     const bool some = x.s != 0.f && t.s != 0.f;
     const double T = a.temperature;
-    a.losses[n] = some ? (float)(T * T * (sum * by / t.s + log((double)x.s / t.s))) : 0.f;
+    const double loss = WARM && warm < INFINITY ? warm : sum * by / t.s + log((double)x.s / t.s);
+    a.losses[n] = some ? (float)(T * T * loss) : 0.f;
     float *o = a.stats + n * 4;
     o[0] = x.m;
     o[1] = x.s;
@@ -201,8 +291,9 @@ __global__ void __launch_bounds__(NT) k_distill(DistillArgs a) {
 // another entry too (adding up over the list for every entry took 118 us instead of
 // 28 for 16,000 rows of 876 with lists of 200).  4,096 rows of 128,256 bfloat16
 // logits, 2.1 GB, take 380 us, 5.5 TB/s, bound by memory; with the table as a word
-// per logit, 32 KB of LDS more, 418.
-template <typename TS, typename TG, int NT, int S, bool STREAM>
+// per logit, 32 KB of LDS more, 418.  WARM (of rows that are one slab: what is listed
+// may be overwritten by another one's workgroup): see above.
+template <typename TS, typename TG, int NT, int S, bool STREAM, bool WARM>
 __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   constexpr int E = sizeof(TS) == 2 && sizeof(TG) == 2 ? 8 : 4;
   constexpr int U = 4;
@@ -211,6 +302,7 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   const int top8 = (a.top + 7) / 8 * 8;
   int32_t *ids = lds;
   float *parts = (float *)(ids + top8), *listed = parts + top8;  // (their logits)
+  float *theirs = listed + top8;                                 // (WARM: the teacher's)
   const int tid = threadIdx.x;
   const uint32_t slabs = (uint32_t)((a.vocab + S - 1) / S);
   const uint32_t row = blockIdx.x / slabs, slab = blockIdx.x - row * slabs;
@@ -236,6 +328,7 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
     ids[j] = y.id;
     parts[j] = y.id >= 0 ? power(y.t - tm, k) * by_ts : 0.f;
     if (place(y.id) < (uint32_t)count) listed[j] = (float)z[place(y.id)];
+    if (WARM) theirs[j] = y.t;
   }
   for (int i = tid; i < S / 32; i += NT) seen[i] = twice[i] = 0;
   if (bad && slab == 0) atomicOr(a.status, BPE_STATUS_BAD_ID);
@@ -245,6 +338,24 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
     for (int e = 0; e < E; ++e) y.v[e] = from_f32<TG>(some ? c * share((float)x.v[e]) : 0.f);
     return y;
   };
+  Near near = {0.0, INFINITY};
+  if (WARM) {
+    __syncthreads();
+    const double by = 1.0 / (double)a.temperature;
+    auto get = [&](int j, float *e, float *f, double *d) {
+      if (place(ids[j]) >= (uint32_t)count) return false;
+      *e = power(theirs[j] - tm, k);
+      *f = power(listed[j] - zm, k);
+      *d = (((double)theirs[j] - tm) - ((double)listed[j] - zm)) * by;
+      return *e != 0.f;
+    };
+    float e, f;
+    double d, held = 0.0;
+    for (int j = tid; j < a.top; j += NT)
+      if (get(j, &e, &f, &d)) held += (double)f;
+    held = group_sum<NT>(held, nullptr);
+    if (some && held > 0.75 * (double)zs) near = near_teacher<TS, NT>(get, a.top, z, count, zm, k, held, nullptr);
+  }
   // (the barrier: the listed logits are read before any is overwritten)
   auto claim = [&] {
     __syncthreads();
@@ -277,6 +388,15 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
     const uint32_t at = place(id);
     if (at >= (uint32_t)count) continue;
     float p = parts[j];
+    if (WARM && near.loss < INFINITY && p != 0.f) {
+      // q - P of this entry, less the other entries' P
+      const double d = (((double)theirs[j] - tm) - ((double)listed[j] - zm)) / (double)a.temperature;
+      double y = (double)p * expm1(near.mean - d - near.loss);
+      if (twice[at >> 5] >> (at & 31) & 1)
+        for (int i = 0; i < a.top; ++i) y -= i != j && ids[i] == id ? (double)parts[i] : 0.0;
+      g[at] = from_f32<TG>(c * (float)y);
+      continue;
+    }
     if (twice[at >> 5] >> (at & 31) & 1) {
       p = 0.f;
       for (int i = 0; i < a.top; i += 8) {
@@ -292,31 +412,36 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   }
 }
 
-template <typename TS>
-hipError_t distill_as(const DistillArgs &a, hipStream_t stream) {
+template <typename TS, int NT>
+hipError_t distill_rows(const DistillArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)a.rows);
-  if (a.vocab <= kDistillNarrow)
-    hipLaunchKernelGGL((k_distill<TS, 64>), grid, dim3(64), 0, stream, a);
+  if (a.temperature > kDistillWarm)
+    hipLaunchKernelGGL((k_distill<TS, NT, true>), grid, dim3(NT), 0, stream, a);
   else
-    hipLaunchKernelGGL((k_distill<TS, kDistillThreads>), grid, dim3(kDistillThreads), 0, stream, a);
+    hipLaunchKernelGGL((k_distill<TS, NT, false>), grid, dim3(NT), 0, stream, a);
   return hipGetLastError();
 }
+template <typename TS>
+hipError_t distill_as(const DistillArgs &a, hipStream_t stream) {
+  return a.vocab <= kDistillNarrow ? distill_rows<TS, 64>(a, stream) : distill_rows<TS, kDistillThreads>(a, stream);
+}
 
-template <typename TS, typename TG, int NT, int S>
+template <typename TS, typename TG, int NT, int S, bool WARM>
 hipError_t grad_slabs(const DistillArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.vocab + S - 1) / S * a.rows));
-  const size_t lds = (a.top + 7) / 8 * 8 * 3 * sizeof(int32_t);
+  const size_t lds = (a.top + 7) / 8 * 8 * (WARM ? 4 : 3) * sizeof(int32_t);
   const bool big = a.rows * a.vocab * (int64_t)sizeof(TG) >= kStreamBytes;
   if (big)
-    hipLaunchKernelGGL((k_distill_grad<TS, TG, NT, S, true>), grid, dim3(NT), lds, stream, a);
+    hipLaunchKernelGGL((k_distill_grad<TS, TG, NT, S, true, WARM>), grid, dim3(NT), lds, stream, a);
   else
-    hipLaunchKernelGGL((k_distill_grad<TS, TG, NT, S, false>), grid, dim3(NT), lds, stream, a);
+    hipLaunchKernelGGL((k_distill_grad<TS, TG, NT, S, false, WARM>), grid, dim3(NT), lds, stream, a);
   return hipGetLastError();
 }
 template <typename TS, typename TG>
 hipError_t grad_launch(const DistillArgs &a, hipStream_t stream) {
-  return a.vocab <= kDistillNarrow ? grad_slabs<TS, TG, 64, kDistillNarrow>(a, stream)
-                                   : grad_slabs<TS, TG, kDistillThreads, kDistillSlab>(a, stream);
+  if (a.vocab > kDistillNarrow) return grad_slabs<TS, TG, kDistillThreads, kDistillSlab, false>(a, stream);
+  return a.temperature > kDistillWarm ? grad_slabs<TS, TG, 64, kDistillNarrow, true>(a, stream)
+                                      : grad_slabs<TS, TG, 64, kDistillNarrow, false>(a, stream);
 }
 template <typename TS>
 hipError_t grad_as(const DistillArgs &a, int gt, hipStream_t stream) {

@@ -258,6 +258,14 @@ constexpr int kDistillThreads = 256;
 // 4.9 and 4.8 (5.2 and 4.5); behind only for the gradient of float32 rows with long
 // lists (16,000 of 876, lists of 200: 45 and 34).
 constexpr int kDistillNarrow = 2048;
+// Temperature above which rows whose list holds most of the student's sum are worked
+// out from the tokens' differences (lm_distill.hip, "warm rows").  Up to it the losses'
+// error of some 2^-23 T^2 stays below 2^-18, and kernels do not ask.  At 4 and above,
+// loss and gradient of bfloat16 logits in us: 16,000 rows of 876, lists of 16 15.8 and
+// 16.4 (16.7 and 18.0), of 200 22.7 and 25.5 (25.8 and 29.4), of all 876, which are such
+// rows, 52 and 139 (91 and 213); 8,000 of 2,048, lists of 16 10.4 and 10.6 (12.7 and
+// 13.0); 4,096 of 50,257 or 128,256 the same.
+constexpr float kDistillWarm = 4.0f;
 
 struct DistillArgs {
   const void *student, *teacher;

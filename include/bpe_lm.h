@@ -362,6 +362,12 @@ int bpe_verify_drafts(const void *d_target, int prob_type, int64_t n_rows, int64
  * all -infinity, has loss 0 and a gradient of zeros.  A term with P_k = 0 is 0,
  * and a P_k below 2^-126 of the largest counts as that; a listed token with another
  * P_k whose z is -infinity makes the loss infinite.
+ * The sums are of 32 bits: a loss is off by some 2^-23 T^2 (more in large
+ * vocabularies, whose sums are long), which matters where it is itself far below
+ * T^2.  At temperatures above 4, where such losses are the rule if the listed tokens
+ * are nearly all that the student gives anything to, rows whose listed tokens hold
+ * more than 3 / 4 of the student's sum are worked out from the tokens' differences
+ * t - z in 64 bits instead, and their losses are off by some 2^-21 of themselves.
  * 2^-20 <= temperature <= 2^20, 0 <= top <= BPE_MAX_TOP, 1 <= vocab <= BPE_MAX_ROWS,
  * n_rows < 2^24.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */
@@ -378,6 +384,9 @@ int bpe_distill(const void *d_student, int student_type, int64_t n_rows, int64_t
  *  d_grad    [n_rows][vocab] of grad_type; may be d_student itself (same type
  *            and stride), else they must not overlap.
  * Rows of loss 0 that bpe_distill names have zeros, whatever dloss is.
+ * An entry of a listed token is off by some 2^-22 of dloss T (softmax + P), or, where
+ * bpe_distill works a row out from differences and vocab is at most 2,048, of
+ * dloss T times the row's typical difference of the two.
  * n_rows * ceil(vocab / 8192) < 2^24.  Returns BPE_OK, BPE_EINVAL or BPE_EHIP.
  */
 int bpe_distill_grad(const void *d_student, int student_type, int64_t n_rows, int64_t vocab,
