@@ -209,7 +209,8 @@ BPE_HD int64_t cache_slot(const int32_t *row, int64_t width, int32_t bs, int64_t
 // The first request in [lo, hi) that ends behind token t, or hi.  In range also
 // for offsets that do not increase.  (Growing steps from lo on would take fewer
 // loads, but hipcc 7.2 miscompiles their 64-bit minimum: the select that it makes
-// for it takes the carry of the sum before it.)
+// for it takes the carry of the sum before it.  tests/test_device_code.py looks for
+// that in all that is built.)
 BPE_HD int64_t cache_request(const int64_t *off, int64_t lo, int64_t hi, int64_t t) {
   while (lo < hi) {
     const int64_t mid = (lo + hi) >> 1;
