@@ -1,7 +1,5 @@
 // lm_cache.hip -- a paged cache held in 8 or 4 bits: tokens quantised into their
 // slots, and read back by block table.
-#include <float.h>
-
 #include "lm_device.h"
 
 namespace bpe {
