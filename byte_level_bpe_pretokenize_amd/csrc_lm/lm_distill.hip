@@ -383,30 +383,45 @@ __global__ void __launch_bounds__(NT) k_distill_grad(DistillArgs a) {
   }
   __syncthreads();
   if (!some) return;
+  // the entries that list a token, in their order
+  auto same_token = [&](int32_t id, auto entry) {
+    for (int i = 0; i < a.top; i += 8) {
+      typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+      const i32x4 lo = *(const i32x4 *)&ids[i], hi = *(const i32x4 *)&ids[i + 4];
+      uint32_t same = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) same |= (uint32_t)(lo[e] == id) << e | (uint32_t)(hi[e] == id) << (e + 4);
+      for (; same; same &= same - 1) entry(i + __ffs(same) - 1);
+    }
+  };
   for (int j = tid; j < a.top; j += NT) {
     const int32_t id = ids[j];
     const uint32_t at = place(id);
     if (at >= (uint32_t)count) continue;
     float p = parts[j];
-    if (WARM && near.loss < INFINITY && p != 0.f) {
-      // q - P of this entry, less the other entries' P
-      const double d = (((double)theirs[j] - tm) - ((double)listed[j] - zm)) / (double)a.temperature;
-      double y = (double)p * expm1(near.mean - d - near.loss);
-      if (twice[at >> 5] >> (at & 31) & 1)
-        for (int i = 0; i < a.top; ++i) y -= i != j && ids[i] == id ? (double)parts[i] : 0.0;
-      g[at] = from_f32<TG>(c * (float)y);
-      continue;
-    }
-    if (twice[at >> 5] >> (at & 31) & 1) {
-      p = 0.f;
-      for (int i = 0; i < a.top; i += 8) {
-        typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-        const i32x4 lo = *(const i32x4 *)&ids[i], hi = *(const i32x4 *)&ids[i + 4];
-        uint32_t same = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) same |= (uint32_t)(lo[e] == id) << e | (uint32_t)(hi[e] == id) << (e + 4);
-        for (; same; same &= same - 1) p += parts[i + __ffs(same) - 1];
+    const bool more = twice[at >> 5] >> (at & 31) & 1;
+    if (WARM && near.loss < INFINITY) {
+      // q - P by the token's first entry that the teacher gives anything to, less its
+      // other entries' P: the same bits from each of them
+      int j0 = parts[j] != 0.f ? j : -1;
+      double others = 0.0;
+      if (more) {
+        j0 = -1;
+        same_token(id, [&](int i) {
+          if (parts[i] == 0.f) return;
+          if (j0 < 0) j0 = i;
+          else others += (double)parts[i];
+        });
       }
+      if (j0 >= 0) {
+        const double d = (((double)theirs[j0] - tm) - ((double)listed[j0] - zm)) / (double)a.temperature;
+        g[at] = from_f32<TG>(c * (float)((double)parts[j0] * expm1(near.mean - d - near.loss) - others));
+        continue;
+      }
+    }
+    if (more) {
+      p = 0.f;
+      same_token(id, [&](int i) { p += parts[i]; });
     }
     g[at] = from_f32<TG>(c * (share(listed[j]) - p));
   }

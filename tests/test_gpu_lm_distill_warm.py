@@ -209,7 +209,13 @@ def test_tokens_listed_more_than_once(T):
     ids[2, 100:104] = ids[2, 9]
     ids[3, ::2] = ids[3, 1::2]           # each of half the tokens twice
     ids[4] = 5
-    check_warm(z, ids, t, T, F32, all_near=False)
+    ids[5, 7:60:2] = ids[5, 6:60:2]      # one of the two, the first or the second, without weight
+    t[5, 6:30:2], t[5, 31:60:2] = -float("inf"), -float("inf")
+    _, got = check_warm(z, ids, t, T, F32, all_near=False)
+    st = lm.distill(z, dev(ids), t, T)[1]
+    dl = torch.randn(10, device=device(), generator=gen(0))
+    for _ in range(3):
+        assert torch.equal(lm.distill_grad(z, dev(ids), t, st, dl, T, out_dtype=F32), got)
     both = np.ascontiguousarray(np.concatenate([ids[:, :200]] * 2, 1))
     check_warm(z[:, :], both, t[:, :200].repeat(1, 2), T, F32, all_near=False)
 
