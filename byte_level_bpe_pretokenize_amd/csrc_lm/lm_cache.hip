@@ -106,10 +106,12 @@ __device__ __forceinline__ void rare(float *y, int m, int lanes, float *scale, f
 // exchange between these lanes, the codes by one multiplication each (the
 // inverse is rounded once per group) instead of a division.
 // A workgroup has whole tokens, about four vectors a thread, whose loads all go
-// first: 60,000 tokens of 16 heads of 128 in bfloat16 to int8, 377 MB, take 75 us,
-// 5.0 TB/s (a copy makes 4.8), bound by memory; one vector at a time, exchanged
-// through LDS and stored by bytes, took 116.  64 tokens: 4.6 us, a chain of three
-// dependent accesses.
+// first: 60,000 tokens of 16 heads of 128 in bfloat16 to int8, 377 MB, take 75 to 81
+// us from run to run, 4.6 to 5.0 TB/s (a copy makes 4.8), bound by memory; one vector
+// at a time, exchanged through LDS and stored by bytes, took 116.  To 4 bits, 315 MB,
+// 76, 4.1 TB/s.  Heads of 77, whose last lanes store bytes: 90 us, 2.5 TB/s (4 bits
+// 97, 2.0); of 96 in groups of 64, a quarter of whose lanes have nothing: 69, 4.1
+// (69, 3.5).  64 tokens: 4.7 us, a chain of three dependent accesses.
 template <typename T, int F, bool WHOLE>
 __global__ void __launch_bounds__(CT) k_cache_write(CacheArgs a) {
   static_assert(E == 8, "group / 8 lanes");
@@ -283,10 +285,12 @@ __device__ __forceinline__ void load_few(const uint8_t *q, int dim, uint32_t *w)
 // A workgroup has up to 64 tokens in a row of the packed batch.  Their slots
 // first, a lane each: the request by the offsets, the block by the table.  Then
 // the tokens' vectors side by side, four a thread, whose loads all go first.
-// 384,000 tokens of 16 heads of 128 from 4 bits to bfloat16, 2.0 GB, take 392 us,
-// 5.1 TB/s, bound by memory (760 with one vector at a time, loaded by bytes).  1,800
-// tokens of 16 heads of 64: 4.4 us, a chain of five dependent accesses.  Heads of no
-// whole vectors: 60,000 tokens of 64 heads of 77 in e4m3 3.5 TB/s, and of 80 4.8.
+// 384,000 tokens of 16 heads of 128 from 4 bits to bfloat16, 2.0 GB, take 395 us,
+// 5.1 TB/s, bound by memory (760 with one vector at a time, loaded by bytes; a
+// profiler's trace, which keeps launches apart, has 439 for the same).  1,800 tokens of
+// 16 heads of 64: 4.5 us, a chain of five dependent accesses.  Heads of no whole
+// vectors: 60,000 tokens of 64 heads of 77 in e4m3 3.9 TB/s (4 bits 2.5), and of 80
+// 5.1 (4.2).
 template <typename T, int F, int N, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(CT) k_cache_read(CacheArgs a) {
   constexpr int64_t kNot = INT64_MIN;  // no request's

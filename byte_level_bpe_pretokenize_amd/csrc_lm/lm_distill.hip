@@ -54,7 +54,8 @@ __device__ __forceinline__ Soft wave_soft(Soft x, float k) {
 
 // Elements of p[0 .. n) before its first 16-byte boundary.  Rows of odd width start
 // anywhere: 4,096 rows of 50,257 bfloat16 logits take 75 us with vectors from the
-// boundary on, 92 from the row's start (float32: no difference; short rows: slower).
+// boundary on, 92 from the row's start (float32: no difference; short rows: slower), of
+// the same logits each time; 83 where two batches are read in turn.
 template <typename T>
 __device__ __forceinline__ int before_16(const T *p, int n) {
   return min(n, (int)((0 - (uintptr_t)p) & 15) / (int)sizeof(T));
@@ -152,9 +153,9 @@ __device__ __forceinline__ Near near_teacher(F get, int top, const TS *z, int V,
 
 // A workgroup per row: one pass over the logits with a running maximum and sum
 // per thread, joined over the workgroup; the listed logits are gathered before.
-// 4,096 rows of 128,256 bfloat16 logits, 1.05 GB, take 182 us, 5.8 TB/s, bound by
+// 4,096 rows of 128,256 bfloat16 logits, 1.05 GB, take 184 us, 5.7 TB/s, bound by
 // memory (the vector instructions alone would take about two thirds of that).  Few
-// rows are bound by what one CU reads: 48 rows of 32,256 6.6 us, one of 128,256 12.5
+// rows are bound by what one CU reads: 48 rows of 32,256 6.6 us, one of 128,256 11.1
 // (workgroups of 1,024 threads were no faster from 1 to 1,500 rows, and slower for
 // many).
 // With e_j = exp((t_j - largest t) / T), the loss is

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kVerifyThreads) k_verify_sums(VerifyArgs a) {
 
 // The next tokens.  ALONE: a workgroup per request, whose waves add up the regions
 // and whose first one draws; else a wave per request, after k_verify_sums.  A chain
-// of dependent accesses: 4.1 us after the sums; alone 6 us for up to 16,384 tokens
+// of dependent accesses: 4.1 us after the sums; alone 6.6 us for up to 16,384 tokens
 // and 11.5 for 50,256 (4 requests; two launches of 4.4 and 4.1).  The drawing is one
 // wave's, by DPP scans without barriers: a workgroup's scans took twice as long.
 template <typename T, bool DRAFT, bool ALONE>
