@@ -263,3 +263,45 @@ def test_against_differences():
     # few U of them, and those of z + s e d, half a step of up to 8 each, by the gradient
     tol = 8 * U * (up.abs() + down.abs()) / (2 * e) + (leaf.grad.double().abs() * 2.0 ** -21).sum(1) / (2 * e)
     assert bool(((slope - want).abs() <= tol + 1e-3 * want.abs() / 1.0).all())
+
+
+@pytest.mark.parametrize("V,K", [(700, 700), (5000, 600)])
+def test_captured_and_replayed_on_another_stream(V, K):
+    """Loss and gradient in one graph, replayed with logits that are near the teacher's, far from
+    them and near again, between eager calls on two streams at once."""
+    T, st, dl = 24.0, status(), torch.ones(9, device=device())
+    z, ids, t = torch.zeros(9, V, device=device()), torch.zeros(9, K, dtype=torch.int32, device=device()), \
+        torch.zeros(9, K, device=device())
+    out = [torch.zeros(9, device=device()), torch.zeros(9, 4, device=device()), torch.zeros(9, V, device=device())]
+
+    def step():
+        lm.distill(z, ids, t, T, losses=out[0], stats=out[1], status=st)
+        lm.distill_grad(z, ids, t, out[1], dl, T, out=out[2], status=st)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for k, noise in enumerate((0.1, 30.0, 0.1, 0.0)):
+        z2, ids2, t2 = all_listed(9, K, noise, F32, F32, 60 + k)
+        z.fill_(-float("inf") if k % 2 == 0 else -50.0)
+        z[:, :K] = z2
+        ids.copy_(dev(ids2))
+        t.copy_(t2)
+        dl.copy_(torch.randn(9, device=device(), generator=gen(k)))
+        graph.replay()
+        torch.cuda.synchronize()
+        loss, ltol, _, _, _ = warm(f64(z), ids2, f64(t), T, f64(dl))
+        check(out[0], loss, ltol, "loss")
+        streams, got = [torch.cuda.Stream() for _ in range(2)], []
+        for _ in range(5):
+            for s in streams:
+                losses, stats = lm.distill(z, ids, t, T, status=st, stream=s)
+                got.append((losses, lm.distill_grad(z, ids, t, stats, dl, T, status=st, stream=s)))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, out[0]) and torch.equal(b, out[2]) for a, b in got)
+    assert int(st.item()) == 0
